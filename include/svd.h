@@ -361,6 +361,150 @@ int svd_select_and_verify_noalloc(const void *p_logits, const void *q_logits,
                                   int32_t *accept_len, int32_t *next_token, float *scores,
                                   float *alpha, float *beta, void *hip_stream);
 
+/*
+ * The operators around a verification step.  One convention serves them all:
+ * prefix b has ctx_len[b] committed tokens in the cache; its tree has up to T
+ * nodes, n_nodes[b] of them used.  Node 0, the root, is the last committed
+ * token (not in the cache yet), the others are drafted tokens, every node after
+ * its parent.  anc [B][T][W], W = ceil(T / 32), holds one bit per node: bit
+ * i % 32 of anc[b][t][i / 32] says that node i is on node t's path, t itself
+ * and the root included.  The verifier's row of node t predicts the token
+ * after t, so the row pool [B * T][V] is what svd_select_and_verify_rows reads.
+ * Limits: 1 <= T <= SVD_MAX_NODES, B * T < 2^30.
+ */
+#define SVD_MAX_NODES 4096
+
+/*
+ * The draft tree of K drafts (SpecDiff-2 appendix B.8: drafts with a common
+ * prefix are flattened into one tree, verified in one pass).  One node per
+ * distinct drafted prefix, numbered draft by draft; a draft ends at its first
+ * negative token.
+ *   drafts  [B][K][gamma] int32
+ *   root    [B] int32, nullable  the last committed token (-1 when NULL)
+ *   tokens  [B][T] out  the node's token;  parent [B][T] out  its parent node,
+ *           -1 for the root;  depth [B][T] out  tokens after the root;
+ *   anc     [B][T][W] out;  n_nodes [B] out  nodes used, root included
+ *   p_index [B][K][gamma+1] out  row of the pool [B * T][V] that scores the
+ *           position: b * T + node of the position before it; -1 past a draft's end
+ * Unused nodes: token -1, parent -1, depth 0, no bits.  T = 1 + K * gamma always
+ * suffices; a prefix with more nodes than T is a data error: n_nodes = -1, its
+ * p_index -1 (so that svd_select_and_verify_rows gives it -1 outputs).
+ */
+int svd_draft_tree(const int32_t *drafts, const int32_t *root, int64_t B, int32_t K, int32_t gamma,
+                   int32_t T, int32_t *tokens, int32_t *parent, int32_t *depth, uint32_t *anc,
+                   int32_t *n_nodes, int32_t *p_index, void *hip_stream);
+
+/*
+ * A paged key/value cache.  k and v are [n_pages][kv_heads][page][head_dim];
+ * position p of sequence b is in page block_table[b][p / page], place p % page.
+ * SVD_CACHE_E4M3 holds 8-bit codes (OCP E4M3) with one power of two per (token,
+ * head) row, the smallest 2^e with max |x| <= 448 * 2^e over the row's finite
+ * values, e in [-126, 120]: k_scale and v_scale [n_pages][kv_heads][page] hold
+ * e + 127 (a byte from 1 to 254).  A value is code * 2^e, exactly, in bf16 too (what
+ * would round to 2^128 is held as 240 * 2^120); an infinity or NaN is held as NaN.  Limits: head_dim 64 or 128; page a power of
+ * two from 16 to 1024; max_pages * page < 2^31; k and v 16-byte aligned.  The
+ * struct is read during the call only.
+ */
+typedef enum {
+  SVD_CACHE_BF16 = 0,
+  SVD_CACHE_E4M3 = 1,
+  SVD_CACHE_RANGE_MIN_ = -2147483647 - 1, /* any int32 is a valid argument, rejected */
+  SVD_CACHE_RANGE_MAX_ = 2147483647       /* (SVD_EDTYPE) unless it names a type */
+} svd_cache_dtype_t;
+typedef struct {
+  void *k, *v;
+  void *k_scale, *v_scale;    /* SVD_CACHE_E4M3 only */
+  const int32_t *block_table; /* [B][max_pages], device */
+  int64_t n_pages;
+  int32_t max_pages, page, kv_heads, head_dim;
+  svd_cache_dtype_t dtype;
+} svd_cache_t;
+
+/*
+ * Write tokens to the cache: token t < n_new[b] of sequence b (n_new nullable:
+ * T) goes to position ctx_len[b] + dst[b][t], or ctx_len[b] + t when dst is
+ * NULL; a negative dst is skipped.  With dst the accepted nodes of a tree are
+ * written again to their committed positions.
+ *   k, v   rows [kv_heads][head_dim] of dtype (SVD_F32 or SVD_BF16); token (b, t)
+ *          starts at element (b * T + t) * k_stride (v_stride)
+ * A position without a page (past max_pages, or a page index outside
+ * [0, n_pages)) is not written.  Two tokens of one call with the same position
+ * leave it with unspecified contents.
+ */
+int svd_cache_write(const svd_cache_t *cache, const void *k, const void *v, svd_dtype_t dtype,
+                    int64_t k_stride, int64_t v_stride, const int32_t *ctx_len,
+                    const int32_t *n_new, const int32_t *dst, int64_t B, int64_t T,
+                    void *hip_stream);
+
+/*
+ * Read positions start[b] (nullable: 0) .. start[b] + count[b] - 1 (count
+ * nullable: N) of every sequence into k, v [B][N][kv_heads][head_dim] of dtype
+ * (16-byte aligned).  Rows from count[b] on are left as they were; a position
+ * without a page gives NaN.
+ */
+int svd_cache_read(const svd_cache_t *cache, const int32_t *start, const int32_t *count, int64_t B,
+                   int64_t N, svd_dtype_t dtype, void *k, void *v, void *hip_stream);
+
+/*
+ * Attention of the tree over the cache (the verifier scores every drafted
+ * position in one parallel pass, SpecDiff-2 section 2; the flattened tree's mask,
+ * appendix B.8).  The keys and values of the nodes are in the cache, node i at
+ * position ctx_len[b] + i (svd_cache_write).  Row (b, t) of query head h attends
+ * to every position below ctx_len[b] and to the nodes of anc[b][t] (anc NULL: a
+ * chain, nodes 0..t), with kv head h / (q_heads / kv_heads):
+ *   out = sum_i softmax_i(scale * q . k_i) v_i,  lse = log sum_i exp(scale * q . k_i)
+ *   q      bf16 rows [q_heads][head_dim]; token (b, t) starts at element
+ *          (b * T + t) * q_stride (a multiple of 8; q 16-byte aligned)
+ *   out    [B][T][q_heads][head_dim] bf16 (16-byte aligned);  lse [B][T][q_heads] fp32, nullable
+ * The running maximum, the sums and the accumulation are fp32; probabilities are
+ * rounded to bf16 as an operand of the second product.  A row that attends to
+ * nothing gives 0 and lse = -inf.  What a row does not attend to does not reach
+ * it, whatever it holds.  Rows from n_nodes[b] on (nullable: T) are left as they
+ * were.  Data errors: with a ctx_len, n_nodes or sum of both out of range every row
+ * of the prefix is NaN; with a page index out of range every row that attends to
+ * a token of that page is.
+ * Workspace: svd_tree_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim,
+ * max_pages * page) bytes (0 for sizes out of range), 256-byte aligned.
+ */
+size_t svd_tree_attention_workspace_bytes(int64_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim, int64_t max_len);
+int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride,
+                       const int32_t *ctx_len, const int32_t *n_nodes, const uint32_t *anc,
+                       float scale, int64_t B, int32_t T, int32_t q_heads, void *out, float *lse,
+                       void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * Penalties, biases and grammar masks on logits [B][T][V], before a sampling or
+ * verification call (V = the verifier's vocabulary; T = 1: plain decoding).  Row
+ * (b, t) predicts the token after node t; its tokens are the history of prefix b
+ * and the nodes on its path (tokens[b][i] for the bits of anc[b][t]; anc NULL: nodes
+ * 0..t; tokens NULL: none).  Ids outside [0, V) are ignored.  In this order, in
+ * fp32, rounded once:
+ *   z > 0 ? z / repetition[b] : z * repetition[b]   for a token that occurs;
+ *   z - frequency[b] * count - presence[b] * [count > 0], count = occurrences
+ *     in history[b][prompt_len[b] ..] (prompt_len nullable: 0) and on the path;
+ *   z + the sum of its entries i in [bias_off[b], bias_off[b+1]) of
+ *     (bias_tok, bias_val)[n_bias];
+ *   -inf where bit v % 32 of allow[allow_index[b][t]][v / 32] is 0
+ *     (allow [n_masks][ceil(V / 32)]; a negative index: no mask).
+ * Each of repetition, frequency, presence [B], history, bias_off, allow is nullable.
+ *   history [B][hist_stride] int32 (hist_stride < 2^30), hist_len [B] of them used
+ *   n_rows  [B] nullable (T): rows from n_rows[b] on are left as they were
+ *   out     [B][T][V]; may be logits itself (only what changes is then moved),
+ *           but must not overlap it otherwise
+ * Values that nothing applies to are copied as they are.  Data errors: a hist_len
+ * or n_rows out of range, or an allow_index >= n_masks, gives NaN rows, which a
+ * verification call reports as -1.  No workspace.
+ */
+int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t B, int32_t T,
+                      int32_t V, const int32_t *n_rows, const int32_t *history,
+                      int64_t hist_stride, const int32_t *hist_len, const int32_t *prompt_len,
+                      const int32_t *tokens, const uint32_t *anc, const float *repetition,
+                      const float *frequency, const float *presence, const int32_t *bias_off,
+                      const int32_t *bias_tok, const float *bias_val, int64_t n_bias,
+                      const uint32_t *allow, const int32_t *allow_index, int32_t n_masks,
+                      void *hip_stream);
+
 /* Static text for a status code. */
 const char *svd_strerror(int status);
 

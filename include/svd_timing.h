@@ -46,7 +46,13 @@ enum {
   SVD_KERNEL_ROWSTATS_LIVE = 13,  /* early exit: slices of the live prefixes' row pairs   */
   SVD_KERNEL_ADL = 14,       /* adaptive draft length: next window per prefix            */
   SVD_KERNEL_BETA_COMBINE = 15, /* split rows: beta from its slices' sums               */
-  SVD_KERNEL_COUNT = 16
+  SVD_KERNEL_DRAFT_TREE = 16,   /* nodes, ancestors and row indices of the draft tree     */
+  SVD_KERNEL_CACHE_WRITE = 17,  /* tokens into the paged cache                            */
+  SVD_KERNEL_CACHE_READ = 18,   /* positions of the paged cache, widened                  */
+  SVD_KERNEL_TREE_ATTENTION = 19, /* attention of the tree over the cache                 */
+  SVD_KERNEL_ATTENTION_JOIN = 20, /* merge of the parts of a split attention              */
+  SVD_KERNEL_ADJUST = 21,       /* penalties, biases and masks on logit rows              */
+  SVD_KERNEL_COUNT = 22
 };
 
 int svd_profile_enable(unsigned kernel_mask);

@@ -9,10 +9,13 @@ arguments take an int address or a tensor):
     svd_workspace_bytes, svd_verify, svd_select_and_verify, svd_greedy_verify,
     svd_greedy_select_and_verify, svd_rows_workspace_bytes, svd_select_and_verify_rows,
     svd_verify_window, svd_cps_workspace_bytes, svd_cps_lattice, svd_cps_beam,
-    svd_adl_next, svd_select_and_verify_noalloc, svd_strerror
+    svd_adl_next, svd_select_and_verify_noalloc, svd_strerror; around the verification step:
+    svd_draft_tree, svd_cache_write, svd_cache_read, svd_tree_attention_workspace_bytes,
+    svd_tree_attention, svd_adjust_logits
 Tensor conveniences that allocate the outputs and the workspace with torch:
     verify, select_and_verify, greedy_verify, greedy_select_and_verify,
-    select_and_verify_rows, verify_window, cps_lattice, cps_beam, adl_next, workspace_bytes
+    select_and_verify_rows, verify_window, cps_lattice, cps_beam, adl_next, workspace_bytes;
+    draft_tree, kv_cache, cache_write, cache_read, tree_attention, adjust_logits
 Kernel timing: timing_library() loads ``libsvd_timed.so`` (the same kernels with
 HIP-event timing compiled in, ``include/svd_timing.h``) as a Library whose raw
 entry points are those above plus svd_profile_enable and svd_profile_read.
@@ -33,20 +36,35 @@ SVD_F32, SVD_BF16 = 0, 1
 SVD_OK, SVD_EINVAL, SVD_EDTYPE, SVD_EWORKSPACE, SVD_EHIP, SVD_ESCRATCH = 0, -1, -2, -3, -4, -5
 SVD_NOALLOC_SCRATCH_BYTES = 16 << 20
 SVD_MAX_K, SVD_MAX_GAMMA = 64, 4096
+SVD_MAX_NODES = 4096
+SVD_CACHE_BF16, SVD_CACHE_E4M3 = 0, 1
 # kernel ids of the timing build (SVD_KERNEL_* in include/svd_timing.h)
 KERNELS = ("rowstats", "select", "draw_pass", "draw_pick", "beta", "mark", "pool_stats",
            "alpha_rows", "lattice", "beam", "lattice_len", "combine", "rowstats_split",
-           "rowstats_live", "adl", "beta_combine")
+           "rowstats_live", "adl", "beta_combine", "draft_tree", "cache_write", "cache_read",
+           "tree_attention", "attention_join", "adjust")
 SVD_RULE_STANDARD, SVD_RULE_GREEDY = 0, 1
 
 C_EXPORTS = ("svd_workspace_bytes", "svd_verify", "svd_select_and_verify", "svd_greedy_verify",
              "svd_greedy_select_and_verify", "svd_rows_workspace_bytes",
              "svd_select_and_verify_rows", "svd_verify_window", "svd_cps_workspace_bytes",
              "svd_cps_lattice", "svd_cps_beam", "svd_adl_next", "svd_select_and_verify_noalloc",
+             "svd_draft_tree", "svd_cache_write", "svd_cache_read",
+             "svd_tree_attention_workspace_bytes", "svd_tree_attention", "svd_adjust_logits",
              "svd_strerror")
 TIMING_EXPORTS = ("svd_profile_enable", "svd_profile_read")
 
 _M64 = 0xFFFFFFFFFFFFFFFF
+
+
+class CacheStruct(ctypes.Structure):
+    """svd_cache_t of include/svd.h; pointers are int addresses."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class SvdError(RuntimeError):
@@ -94,6 +112,20 @@ def _declare(L: ctypes.CDLL, timing: bool) -> ctypes.CDLL:
     L.svd_select_and_verify_noalloc.restype = ctypes.c_int
     L.svd_select_and_verify_noalloc.argtypes = [vp, vp, vp, ctypes.c_int, i64, i32, i32, i32, f32,
                                                 f32, u64, u64, vp, vp, vp, vp, vp, vp, vp]
+    L.svd_draft_tree.restype = ctypes.c_int
+    L.svd_draft_tree.argtypes = [vp, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.svd_cache_write.restype = ctypes.c_int
+    L.svd_cache_write.argtypes = [vp, vp, vp, ctypes.c_int, i64, i64, vp, vp, vp, i64, i64, vp]
+    L.svd_cache_read.restype = ctypes.c_int
+    L.svd_cache_read.argtypes = [vp, vp, vp, i64, i64, ctypes.c_int, vp, vp, vp]
+    L.svd_tree_attention_workspace_bytes.restype = sz
+    L.svd_tree_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i64]
+    L.svd_tree_attention.restype = ctypes.c_int
+    L.svd_tree_attention.argtypes = [vp, vp, i64, vp, vp, vp, f32, i64, i32, i32, vp, vp, vp, sz,
+                                     vp]
+    L.svd_adjust_logits.restype = ctypes.c_int
+    L.svd_adjust_logits.argtypes = [vp, vp, ctypes.c_int, i64, i32, i32, vp, vp, i64, vp, vp, vp,
+                                    vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, i32, vp]
     L.svd_strerror.restype = ctypes.c_char_p
     L.svd_strerror.argtypes = [ctypes.c_int]
     if timing:
@@ -111,6 +143,11 @@ def _addr(x):
     if isinstance(x, int):
         return x
     return x.data_ptr()
+
+
+def _struct(c):
+    """Address of a CacheStruct, or None."""
+    return None if c is None else ctypes.addressof(c)
 
 
 class Library:
@@ -224,6 +261,47 @@ class Library:
             int(row_base) & _M64, _addr(selected), _addr(accept_len), _addr(next_token),
             _addr(scores), _addr(alpha), _addr(beta), _addr(hip_stream)))
 
+    def svd_draft_tree(self, drafts, root, B, K, gamma, T, tokens, parent, depth, anc, n_nodes,
+                       p_index, hip_stream) -> int:
+        return int(self._lib.svd_draft_tree(
+            _addr(drafts), _addr(root), int(B), int(K), int(gamma), int(T), _addr(tokens),
+            _addr(parent), _addr(depth), _addr(anc), _addr(n_nodes), _addr(p_index),
+            _addr(hip_stream)))
+
+    def svd_cache_write(self, cache, k, v, dtype, k_stride, v_stride, ctx_len, n_new, dst, B, T,
+                        hip_stream) -> int:
+        return int(self._lib.svd_cache_write(
+            _struct(cache), _addr(k), _addr(v), int(dtype), int(k_stride), int(v_stride),
+            _addr(ctx_len), _addr(n_new), _addr(dst), int(B), int(T), _addr(hip_stream)))
+
+    def svd_cache_read(self, cache, start, count, B, N, dtype, k, v, hip_stream) -> int:
+        return int(self._lib.svd_cache_read(
+            _struct(cache), _addr(start), _addr(count), int(B), int(N), int(dtype), _addr(k),
+            _addr(v), _addr(hip_stream)))
+
+    def svd_tree_attention_workspace_bytes(self, B: int, T: int, q_heads: int, kv_heads: int,
+                                           head_dim: int, max_len: int) -> int:
+        return int(self._lib.svd_tree_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim,
+                                                                max_len))
+
+    def svd_tree_attention(self, cache, q, q_stride, ctx_len, n_nodes, anc, scale, B, T, q_heads,
+                           out, lse, workspace, workspace_bytes, hip_stream) -> int:
+        return int(self._lib.svd_tree_attention(
+            _struct(cache), _addr(q), int(q_stride), _addr(ctx_len), _addr(n_nodes), _addr(anc),
+            float(scale), int(B), int(T), int(q_heads), _addr(out), _addr(lse), _addr(workspace),
+            int(workspace_bytes), _addr(hip_stream)))
+
+    def svd_adjust_logits(self, logits, out, dtype, B, T, V, n_rows, history, hist_stride,
+                          hist_len, prompt_len, tokens, anc, repetition, frequency, presence,
+                          bias_off, bias_tok, bias_val, n_bias, allow, allow_index, n_masks,
+                          hip_stream) -> int:
+        return int(self._lib.svd_adjust_logits(
+            _addr(logits), _addr(out), int(dtype), int(B), int(T), int(V), _addr(n_rows),
+            _addr(history), int(hist_stride), _addr(hist_len), _addr(prompt_len), _addr(tokens),
+            _addr(anc), _addr(repetition), _addr(frequency), _addr(presence), _addr(bias_off),
+            _addr(bias_tok), _addr(bias_val), int(n_bias), _addr(allow), _addr(allow_index),
+            int(n_masks), _addr(hip_stream)))
+
     def svd_strerror(self, status: int) -> str:
         return self._lib.svd_strerror(int(status)).decode()
 
@@ -278,6 +356,12 @@ svd_cps_lattice = _default.svd_cps_lattice
 svd_cps_beam = _default.svd_cps_beam
 svd_select_and_verify_noalloc = _default.svd_select_and_verify_noalloc
 svd_adl_next = _default.svd_adl_next
+svd_draft_tree = _default.svd_draft_tree
+svd_cache_write = _default.svd_cache_write
+svd_cache_read = _default.svd_cache_read
+svd_tree_attention_workspace_bytes = _default.svd_tree_attention_workspace_bytes
+svd_tree_attention = _default.svd_tree_attention
+svd_adjust_logits = _default.svd_adjust_logits
 svd_strerror = _default.svd_strerror
 
 
@@ -607,3 +691,294 @@ def adl_next(drafts, selected, accept_len, avg, gamma_b=None, eos=-1, k_min=1, k
     if rc != SVD_OK:
         raise SvdError(rc, "svd_adl_next")
     return nxt
+
+
+# --------------------------------------------------------------------------
+# Around the verification step: the draft tree, the paged cache, the attention
+# of the tree over it, and the adjustments of the verifier's logits
+
+def _ints(dev, **tensors):
+    """Check int32 tensors (None is allowed) and where they are."""
+    import torch
+    for n, t in tensors.items():
+        if t is None:
+            continue
+        _check(t, n, dev)
+        if t.dtype != torch.int32:
+            raise TypeError("%s must be int32" % n)
+
+
+def _shaped(shape, **tensors):
+    for n, t in tensors.items():
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must be %s, got %s" % (n, list(shape), list(t.shape)))
+
+
+def _on(dev, stream):
+    """The stream's handle (default: the device's current one)."""
+    import torch
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+
+
+def _call_on(dev, f, *args):
+    """f(*args) with dev as the current device."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
+def draft_tree(drafts, root=None, n_max=None, stream=None):
+    """The prefix tree of drafts [B,K,gamma] int32: root [B] int32 the last
+    committed tokens, n_max room for nodes (default 1 + K * gamma, which always
+    suffices).  Returns tokens, parent, depth [B,n_max], anc [B,n_max,W] (bit i % 32
+    of word i // 32: node i is on the node's path), n_nodes [B] and p_index
+    [B,K,gamma+1], the rows of the pool [B * n_max, V] for select_and_verify_rows."""
+    import torch
+    dev = drafts.device
+    _ints(dev, drafts=drafts, root=root)
+    if drafts.dim() != 3:
+        raise ValueError("drafts must be [B,K,gamma]")
+    B, K, G = drafts.shape
+    _shaped((B,), root=root)
+    T = 1 + K * G if n_max is None else int(n_max)
+    W = (T + 31) // 32
+    flat = torch.empty(B * (3 * T + T * W + 1 + K * (G + 1)) if T > 0 else 0, dtype=torch.int32,
+                       device=dev)
+    out, at = {}, 0
+    for name, shape in (("tokens", (B, T)), ("parent", (B, T)), ("depth", (B, T)),
+                        ("anc", (B, T, W)), ("n_nodes", (B,)), ("p_index", (B, K, G + 1))):
+        n = 1
+        for d in shape:
+            n *= d
+        out[name] = flat[at:at + n].view(shape) if T > 0 else flat
+        at += n
+    rc = _call_on(dev, svd_draft_tree, drafts, root, B, K, G, T, out["tokens"], out["parent"],
+                  out["depth"], out["anc"], out["n_nodes"], out["p_index"], _on(dev, stream))
+    if rc != SVD_OK:
+        raise SvdError(rc, "svd_draft_tree")
+    return out
+
+
+def kv_cache(n_pages, kv_heads, page, head_dim, dtype=None, device="cuda"):
+    """An empty paged cache: k and v [n_pages,kv_heads,page,head_dim] of
+    torch.bfloat16 (the default) or torch.float8_e4m3fn, and for the latter
+    k_scale and v_scale [n_pages,kv_heads,page] uint8 (exponent + 127)."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("a cache is torch.bfloat16 or torch.float8_e4m3fn, got %s" % dtype)
+    c = {n: torch.zeros((n_pages, kv_heads, page, head_dim), dtype=dtype, device=device)
+         for n in ("k", "v")}
+    for n in ("k_scale", "v_scale"):
+        c[n] = (None if dtype == torch.bfloat16 else
+                torch.full((n_pages, kv_heads, page), 127, dtype=torch.uint8, device=device))
+    return c
+
+
+def _cache_struct(cache, block_table, B):
+    import torch
+    k, v, ks, vs = cache["k"], cache["v"], cache.get("k_scale"), cache.get("v_scale")
+    dev = k.device
+    for t, n in ((k, "cache k"), (v, "cache v")):
+        _check(t, n, dev)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("cache k and v must be [n_pages,kv_heads,page,head_dim] of one dtype")
+    if k.dtype == torch.bfloat16:
+        code, ks, vs = SVD_CACHE_BF16, None, None
+    elif k.dtype == torch.float8_e4m3fn:
+        code = SVD_CACHE_E4M3
+        for t, n in ((ks, "cache k_scale"), (vs, "cache v_scale")):
+            if t is None or t.dtype != torch.uint8:
+                raise TypeError("%s must be uint8" % n)
+            _check(t, n, dev)
+            if t.shape != k.shape[:3]:
+                raise ValueError("%s must be [n_pages,kv_heads,page]" % n)
+    else:
+        raise TypeError("a cache is torch.bfloat16 or torch.float8_e4m3fn, got %s" % k.dtype)
+    _ints(dev, block_table=block_table)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B,max_pages]")
+    n_pages, heads, page, D = k.shape
+    return CacheStruct(_addr(k), _addr(v), _addr(ks), _addr(vs), _addr(block_table), n_pages,
+                       block_table.shape[1], page, heads, D, code)
+
+
+def _token_stride(t, name, heads, D, dev):
+    """Elements between the tokens of t [B,T,heads,D], whose heads are contiguous."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev))
+    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != D:
+        raise ValueError("%s must be [B,T,%d,%d], got %s" % (name, heads, D, list(t.shape)))
+    B, T = t.shape[:2]
+    sb, st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (heads > 1 and sh != D):
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    if T == 1:
+        st = sb if B > 1 else heads * D
+    elif B > 1 and sb != T * st:
+        raise ValueError("the tokens of %s must be evenly strided" % name)
+    return st
+
+
+def cache_write(cache, k, v, block_table, ctx_len, n_new=None, dst=None, stream=None):
+    """Write k, v [B,T,kv_heads,D] (bf16 or fp32; the tokens may be strided, as in
+    a fused projection) to positions ctx_len[b] + t, or ctx_len[b] + dst[b,t] where
+    dst is not negative; n_new [B] limits the tokens of a sequence.  cache: as from
+    kv_cache; block_table [B,max_pages], ctx_len [B], dst [B,T] int32."""
+    dev = cache["k"].device
+    B, T = k.shape[:2]
+    c = _cache_struct(cache, block_table, B)
+    ks = _token_stride(k, "k", c.kv_heads, c.head_dim, dev)
+    vs = _token_stride(v, "v", c.kv_heads, c.head_dim, dev)
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must share one shape and dtype")
+    _ints(dev, ctx_len=ctx_len, n_new=n_new, dst=dst)
+    _shaped((B,), ctx_len=ctx_len, n_new=n_new)
+    _shaped((B, T), dst=dst)
+    rc = _call_on(dev, svd_cache_write, c, k, v, _dtype_code(k), ks, vs, ctx_len, n_new, dst, B, T,
+                  _on(dev, stream))
+    if rc != SVD_OK:
+        raise SvdError(rc, "svd_cache_write")
+
+
+def cache_read(cache, block_table, n, start=None, count=None, dtype=None, out=None, stream=None):
+    """Positions start[b] .. start[b] + n - 1 of every sequence as (k, v), each
+    [B,n,kv_heads,D] of dtype (default torch.bfloat16, or torch.float32).  count
+    [B] limits a sequence; the rows behind it are left as out = (k, v) has them."""
+    import torch
+    dev = cache["k"].device
+    B = block_table.shape[0]
+    c = _cache_struct(cache, block_table, B)
+    _ints(dev, start=start, count=count)
+    _shaped((B,), start=start, count=count)
+    shape = (B, n, c.kv_heads, c.head_dim)
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        out = tuple(torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
+    k, v = out
+    for t, name in ((k, "out k"), (v, "out v")):
+        _check(t, name, dev)
+    if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+        raise TypeError("out k and v must share the asked dtype")
+    _shaped(shape, k=k, v=v)
+    rc = _call_on(dev, svd_cache_read, c, start, count, B, n, _dtype_code(k), k, v,
+                  _on(dev, stream))
+    if rc != SVD_OK:
+        raise SvdError(rc, "svd_cache_read")
+    return k, v
+
+
+def tree_attention_workspace(B, T, q_heads, cache, block_table):
+    """A workspace for tree_attention calls of these sizes."""
+    import torch
+    k = cache["k"]
+    n = svd_tree_attention_workspace_bytes(B, T, q_heads, k.shape[1], k.shape[3],
+                                           block_table.shape[1] * k.shape[2])
+    if n == 0:
+        raise ValueError("sizes out of range: B=%d T=%d q_heads=%d cache %s" %
+                         (B, T, q_heads, list(k.shape)))
+    return torch.empty(n, dtype=torch.uint8, device=k.device)
+
+
+def tree_attention(q, cache, block_table, ctx_len, anc=None, n_nodes=None, scale=None, out=None,
+                   lse=None, want_lse=False, workspace=None, stream=None):
+    """q [B,T,q_heads,D] bf16 (the tokens may be strided) over the cache: node t of
+    sequence b attends to the ctx_len[b] cached tokens and the nodes of anc[b,t]
+    (None: a chain, nodes 0..t), whose keys and values cache_write has put at
+    positions ctx_len[b] + node.  scale: default D ** -0.5.  Returns out
+    [B,T,q_heads,D] bf16 and, when asked for or given, lse [B,T,q_heads] fp32; rows
+    from n_nodes[b] on are left as out and lse have them."""
+    import torch
+    dev = cache["k"].device
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16, got %s" % q.dtype)
+    if q.dim() != 4:
+        raise ValueError("q must be [B,T,q_heads,D]")
+    B, T, Hq, D = q.shape
+    c = _cache_struct(cache, block_table, B)
+    qs = _token_stride(q, "q", Hq, c.head_dim, dev)
+    if Hq % c.kv_heads != 0:
+        raise ValueError("q_heads must be a multiple of the cache's kv_heads")
+    _ints(dev, ctx_len=ctx_len, anc=anc, n_nodes=n_nodes)
+    _shaped((B,), ctx_len=ctx_len, n_nodes=n_nodes)
+    _shaped((B, T, (T + 31) // 32), anc=anc)
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
+    for t, name, dt in ((out, "out", torch.bfloat16), (lse, "lse", torch.float32)):
+        if t is not None:
+            _check(t, name, dev)
+            if t.dtype != dt:
+                raise TypeError("%s must be %s" % (name, dt))
+    _shaped((B, T, Hq, D), out=out)
+    _shaped((B, T, Hq), lse=lse)
+    if workspace is None:
+        workspace = tree_attention_workspace(B, T, Hq, cache, block_table)
+    rc = _call_on(dev, svd_tree_attention, c, q, qs, ctx_len, n_nodes, anc,
+                  D ** -0.5 if scale is None else scale, B, T, Hq, out, lse, workspace,
+                  workspace.numel(), _on(dev, stream))
+    if rc != SVD_OK:
+        raise SvdError(rc, "svd_tree_attention")
+    return {"out": out, "lse": lse}
+
+
+def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=None, anc=None,
+                  n_rows=None, repetition=None, frequency=None, presence=None, bias=None,
+                  allow=None, allow_index=None, out=None, stream=None):
+    """Penalties, biases and grammar masks on logits [B,T,V] (bf16 or fp32), row
+    (b, t) after node t of a tree.  history [B,H] int32 with hist_len [B] tokens
+    used (prompt_len [B] of them the prompt), tokens [B,T] and anc [B,T,W] of the
+    tree; repetition, frequency, presence [B] fp32; bias = (offsets [B+1] int32,
+    tokens int32, values fp32); allow [n,ceil(V/32)] int32 bit masks and
+    allow_index [B,T] int32 (negative: none).  out: default a new tensor; logits
+    itself for a change in place.  Returns out."""
+    import torch
+    dev = logits.device
+    _check(logits, "logits", dev)
+    code = _dtype_code(logits)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B,T,V]")
+    B, T, V = logits.shape
+    _ints(dev, history=history, hist_len=hist_len, prompt_len=prompt_len, tokens=tokens, anc=anc,
+          n_rows=n_rows, allow=allow, allow_index=allow_index)
+    if history is not None and (history.dim() != 2 or history.shape[0] != B or hist_len is None):
+        raise ValueError("history must be [B,H], with hist_len")
+    _shaped((B,), hist_len=hist_len, prompt_len=prompt_len, n_rows=n_rows, repetition=repetition,
+            frequency=frequency, presence=presence)
+    _shaped((B, T), tokens=tokens, allow_index=allow_index)
+    _shaped((B, T, (T + 31) // 32), anc=anc)
+    for n, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+        if t is not None:
+            _check(t, n, dev)
+            if t.dtype != torch.float32:
+                raise TypeError("%s must be float32" % n)
+    off = tok = val = None
+    if bias is not None:
+        off, tok, val = bias
+        _ints(dev, bias_offsets=off, bias_tokens=tok)
+        _check(val, "bias values", dev)
+        if val.dtype != torch.float32:
+            raise TypeError("bias values must be float32")
+        _shaped((B + 1,), bias_offsets=off)
+        if tok.dim() != 1 or tok.shape != val.shape:
+            raise ValueError("bias tokens and values must be one length")
+    if allow is not None:
+        if allow.dim() != 2 or allow.shape[1] != (V + 31) // 32 or allow_index is None:
+            raise ValueError("allow must be [n,ceil(V/32)], with allow_index")
+    if out is None:
+        out = torch.empty_like(logits)
+    _check(out, "out", dev)
+    _shaped((B, T, V), out=out)
+    if out.dtype != logits.dtype:
+        raise TypeError("out must have the dtype of logits")
+    H = 0 if history is None else history.shape[1]
+    rc = _call_on(dev, svd_adjust_logits, logits, out, code, B, T, V, n_rows,
+                  history if H else None, H, hist_len, prompt_len, tokens, anc, repetition,
+                  frequency, presence, off, tok, val, 0 if tok is None else tok.numel(), allow,
+                  allow_index, 0 if allow is None else allow.shape[0], _on(dev, stream))
+    if rc != SVD_OK:
+        raise SvdError(rc, "svd_adjust_logits")
+    return out

@@ -11,14 +11,18 @@
 #include "svd.h"
 #include "svd_timing.h"
 #include "svd_timing.hpp"
+#include "kr_adjust.hpp"
 #include "kr_adl.hpp"
+#include "kr_attn.hpp"
 #include "kr_beam.hpp"
 #include "kr_beta.hpp"
+#include "kr_cache.hpp"
 #include "kr_cps.hpp"
 #include "kr_draw.hpp"
 #include "kr_rows.hpp"
 #include "kr_rowstats.hpp"
 #include "kr_select.hpp"
+#include "kr_tree.hpp"
 
 namespace {
 
@@ -851,3 +855,5 @@ const char *svd_strerror(int status) {
 }
 
 }  // extern "C"
+
+#include "svd_step.hpp"
