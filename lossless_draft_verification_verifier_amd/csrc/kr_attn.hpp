@@ -25,6 +25,7 @@
 #pragma once
 
 #include "kr_cache.hpp"
+#include "kr_tree.hpp"
 #include "svd_device.hpp"
 
 namespace svd {

@@ -21,6 +21,13 @@ constexpr int kTreeBlock = 512;
 constexpr int kTreeMaxK = 64;
 constexpr int kTreeLdsTokens = 4096;  // drafts of at most this many tokens are staged in LDS
 
+// bits [lo, hi] of a bitmap that fall into word w
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
+  const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 31);
+  if (a > b) return 0;
+  return (0xffffffffu << a) & (0xffffffffu >> (31 - b));
+}
+
 // One workgroup per prefix; see svd_draft_tree for the arrays.
 __global__ __launch_bounds__(kTreeBlock) void kr_draft_tree(
     const int32_t *__restrict__ drafts, const int32_t *__restrict__ root, int K, int G, int T,

@@ -205,14 +205,6 @@ __device__ __forceinline__ int block_min_i(int v, int *lds /* NW + 1 */) {
 }
 
 // ---------------------------------------------------------------------------
-// bits [lo, hi] of a bitmap that fall into word w
-__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
-  const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 31);
-  if (a > b) return 0;
-  return (0xffffffffu << a) & (0xffffffffu >> (31 - b));
-}
-
-// ---------------------------------------------------------------------------
 // Workspace records.
 
 struct RowStats {      // one scored row pair
