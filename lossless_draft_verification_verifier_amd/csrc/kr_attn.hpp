@@ -1,27 +1,29 @@
 // kr_attn.hpp -- attention of a draft tree over the paged cache.
 //
 // Row r = t * group + i of kv head h is query head h * group + i of node t; all
-// rows of a (prefix, kv head) read the same keys and values.  A wave holds
-// 16 * NT rows and walks tiles of 32 cached tokens with the running maximum m
-// and sum l of the softmax:
+// rows of a (prefix, kv head) read the same keys and values.  With the running
+// maximum m and sum l of the softmax, per 32 cached tokens:
 //   S^T = K Q^T         v_mfma_f32_16x16x32_bf16, tokens x rows
 //   p = exp2(S c - m c), c = scale * log2(e)
 //   O^T += V^T P^T      the same instruction, head dimension x rows
 // In the transposed products a lane keeps one row (lane % 16) throughout: the
 // maximum over tokens is in-lane plus two shuffles, the rescaling of O is a
 // per-lane factor, and the p that the first product leaves in a lane are the
-// operand the second one wants there, so p never crosses lanes.  The order of
-// the reduction index is free as long as both operands share it; it is chosen
-// so that every load of K and V is 16 bytes of one token's row, and V is
-// transposed in registers (one byte permute per two elements).
-// E4M3 rows are widened to bf16 with their power of two by the conversion
-// instruction, which is exact, so both cache types run the same products.
+// operand the second one wants there, so p never crosses lanes.
+//
+// A workgroup of 4 waves takes 16 * NT * WQ rows and walks tiles of TK tokens:
+// every thread loads its share of the next tile into registers while the
+// current one is computed from LDS.  Writing the tile to LDS widens E4M3 rows to bf16
+// with their power of two (exact, by the conversion instruction) and transposes
+// V, once for all rows.  WQ waves split the rows; where there are few, WT =
+// 4 / WQ waves split the tile's tokens and merge at the end.  LDS rows hold 16-byte
+// blocks at an index xor'ed with the row, so that 16 lanes reading 16 rows
+// touch all banks.
 // p is rounded to bf16 once, as the operand of the second product; m, l and O
 // stay in 32 bits and l sums the unrounded p.
 //
-// The tiles of a prefix (its context, then its tree) are split evenly over S
-// workgroups when there are few (prefix, head) pairs, and over the 4 waves of
-// a workgroup; kr_attn_join merges the S parts.
+// The tiles of a prefix are split evenly over S workgroups when there are few
+// (prefix, head) pairs; kr_attn_join merges the S parts.
 #pragma once
 
 #include "kr_cache.hpp"
@@ -33,16 +35,16 @@ namespace svd {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef vec16 u32x4;
 
 constexpr int kAttnBlock = 256;
 constexpr int kAttnWaves = kAttnBlock / 64;
-constexpr int kAttnTile = 32;       // cached tokens per step of a wave
 constexpr int kAttnMaxSplits = 64;
 
 struct AttnArgs {
   const uint16_t *q;        // [B][T][Hq][D] bf16, q_stride elements between tokens
   int64_t q_stride;
-  const int32_t *ctx_len, *n_nodes;
+  const int32_t *ctx_len, *n_nodes, *table;
   const uint32_t *anc;      // [B][T][W] or null: a chain
   int64_t room;             // positions of a sequence's pages
   int T, group, S, m_tiles, units;  // units = B * Hkv * S
@@ -65,207 +67,6 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, kHigh));
 }
 
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {  // a bf16 pair that holds NaN or inf
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const vec16 x = *reinterpret_cast<const vec16 *>(p + 4 * i);
-      w[i] = x.x;
-      w[i + 1] = x.y;
-      w[i + 2] = x.z;
-      w[i + 3] = x.w;
-    }
-  } else if constexpr (N == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
-    w[0] = x.x;
-    w[1] = x.y;
-  } else {
-    static_assert(N == 1, "");
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
-  }
-}
-
-// The state of a wave: NT groups of 16 rows.
-template <int D, int NT>
-struct AttnState {
-  static constexpr int DT = D / 16;
-  f32x4 o[NT][DT];
-  float m[NT], l[NT];
-  float base[NT];  // m * c as rounded: the exponent that l and o are held over
-};
-
-// One tile of 32 tokens.  row_k[2]: the cache rows of tokens lane % 16 and
-// 16 + lane % 16; row_v[8]: of tokens 4 g + i and 16 + 4 g + i, g = lane / 16.
-// A row of -1 is a token that is not there (v is taken as zero).  allow[n]: bits of
-// the tile's tokens that row 16 n + lane % 16 attends to.
-template <int D, bool kE4M3, int NT, bool kTree>
-__device__ __forceinline__ void attn_tile(const CacheView &cv, const vec16 (&qf)[NT][D / 32],
-                                          const int64_t (&row_k)[2], const int64_t (&row_v)[8],
-                                          const uint32_t (&allow)[NT], bool all, bool poison,
-                                          float c, AttnState<D, NT> &st) {
-  constexpr int DT = D / 16, ST = D / 32;
-  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  // keys
-  vec16 kf[2][ST];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int64_t row = row_k[s] < 0 ? 0 : row_k[s];
-    if constexpr (kE4M3) {
-      const float sc = pow2_of_scale(cv.k_scale[row]);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const vec16 w = *reinterpret_cast<const vec16 *>(cv.k + row * D + 64 * i + 16 * g);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = h ? w.z : w.x, b = h ? w.w : w.y;
-          kf[s][2 * i + h].x = widen2<false>(a, sc);
-          kf[s][2 * i + h].y = widen2<true>(a, sc);
-          kf[s][2 * i + h].z = widen2<false>(b, sc);
-          kf[s][2 * i + h].w = widen2<true>(b, sc);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < ST; ++i)
-        kf[s][i] = *reinterpret_cast<const vec16 *>(cv.k + (row * D + 32 * i + 8 * g) * 2);
-    }
-  }
-  // values, as pairs of neighbouring head dimensions of one token
-  uint32_t vr[8][DT / 2];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t row = row_v[j] < 0 ? 0 : row_v[j];
-    if constexpr (kE4M3) {
-      const float sc = pow2_of_scale(cv.v_scale[row]);
-      uint32_t w[DT / 4];
-      load_words<DT / 4>(cv.v + row * D + DT * n, w);
-#pragma unroll
-      for (int i = 0; i < DT / 4; ++i) {
-        vr[j][2 * i] = widen2<false>(w[i], sc);
-        vr[j][2 * i + 1] = widen2<true>(w[i], sc);
-      }
-    } else {
-      load_words<DT / 2>(cv.v + (row * D + DT * n) * 2, vr[j]);
-    }
-    if (row_v[j] < 0) {
-#pragma unroll
-      for (int i = 0; i < DT / 2; ++i) vr[j][i] = 0;
-    }
-  }
-  // a masked p is 0, and 0 * NaN is NaN: values that are not finite leave the
-  // product and join the rows that attend to them one by one
-  bool odd = false;
-  if constexpr (kTree) {
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int i = 0; i < DT / 2; ++i) any |= nonfinite2(vr[j][i]);
-    odd = __any(any);
-    if (odd) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < DT / 2; ++i) {
-          if ((vr[j][i] & 0x7f80u) == 0x7f80u) vr[j][i] &= 0xffff0000u;
-          if ((vr[j][i] & 0x7f800000u) == 0x7f800000u) vr[j][i] &= 0x0000ffffu;
-        }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    f32x4 s[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < ST; ++i) s[u] = mfma_bf16(kf[u][i], qf[t][i], s[u]);
-    }
-    if (poison) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[u][r] = __uint_as_float(0x7fc00000u);
-    }
-    if (!all) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (!((allow[t] >> (16 * u + 4 * g + r)) & 1u)) s[u][r] = kNegInf;
-    }
-    float mx = st.m[t];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[u][r]);
-    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    if (__any(mx != st.m[t])) {
-      const float next = mx * c;
-      const float f = mx == st.m[t] ? 1.0f : fast_exp2(st.base[t] - next);
-      st.l[t] *= f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) st.o[t][i] *= f;
-      st.m[t] = mx;
-      st.base[t] = next;
-    }
-    const float base = mx == kNegInf ? 0.0f : st.base[t];
-    float p[8];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        p[4 * u + r] = fast_exp2(__builtin_fmaf(s[u][r], c, -base));
-        st.l[t] += p[4 * u + r];
-      }
-    vec16 pf;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) pf[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
-#pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      vec16 vf;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        vf[j] = __builtin_amdgcn_perm(vr[2 * j + 1][i / 2], vr[2 * j][i / 2],
-                                      (i & 1) ? 0x07060302u : 0x05040100u);
-      st.o[t][i] = mfma_bf16(vf, pf, st.o[t][i]);
-    }
-    if constexpr (kTree) {
-      if (odd) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          for (int from = 0; from < 4; ++from) {
-            const int tok = 16 * (j >> 2) + 4 * from + (j & 3);
-            const float pt = __shfl(p[j], 16 * from + n, 64);
-            const uint32_t hi = __shfl((uint32_t)((uint64_t)row_v[j] >> 32), 16 * from, 64);
-            const uint32_t lo = __shfl((uint32_t)row_v[j], 16 * from, 64);
-            const int64_t row = (int64_t)(((uint64_t)hi << 32) | lo);
-            if (row < 0 || !((allow[t] >> tok) & 1u)) continue;
-            const float sc = kE4M3 ? pow2_of_scale(cv.v_scale[row]) : 1.0f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int i = 0; i < DT; ++i) {
-                const int64_t at = row * D + DT * (4 * g + r) + i;
-                float x;
-                if constexpr (kE4M3)
-                  x = __builtin_amdgcn_cvt_f32_fp8((uint32_t)cv.v[at], 0) * sc;
-                else
-                  x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(cv.v)[at] << 16);
-                if (!(fabsf(x) < __builtin_huge_valf())) st.o[t][i][r] += pt * x;
-              }
-          }
-      }
-    }
-  }
-}
-
 // What a part (exponent m, sum l) is scaled by under the common exponent mm.  A
 // part without scores has l = 0; one whose scores were all NaN has no maximum
 // either, and its NaN sum has to stay.
@@ -278,11 +79,65 @@ __device__ __forceinline__ bool attn_bad(int ctx, int nodes, int T, int64_t room
   return ctx < 0 || nodes < 0 || nodes > T || (int64_t)ctx + nodes > room;
 }
 
-template <int D, bool kE4M3, int NT>
-__global__ __launch_bounds__(kAttnBlock) void kr_tree_attention(CacheView cv, AttnArgs a) {
-  constexpr int DT = D / 16, ST = D / 32, M = 16 * NT;
-  __shared__ float lds_ms[kAttnWaves][M][2];
-  __shared__ float lds_o[kAttnWaves][M][D + 4];  // + 4: rows start in different banks
+// 4 elements of an output row: o over its sum, and the row's log-sum.
+template <int D>
+__device__ __forceinline__ void attn_row_out(const AttnArgs &a, int64_t row, int d, f32x4 o, float m,
+                                             float l, bool first) {
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that attends to nothing is 0
+  u32x2 w;
+  w.x = pack_bf16(o[0] * inv, o[1] * inv);
+  w.y = pack_bf16(o[2] * inv, o[3] * inv);
+  *reinterpret_cast<u32x2 *>(a.out + row * D + d) = w;
+  if (first && a.lse)
+    a.lse[row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
+// 32 bits of node t's ancestors from bit i0 on; bits below 0 are context, which
+// every row attends to.  words null: a chain.
+__device__ __forceinline__ uint32_t allow_window(const uint32_t *words, int W, int t, int i0) {
+  if (!words) {
+    const int last = t - i0;  // tokens up to the node itself
+    return last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
+  }
+  if (i0 <= -32) return 0xffffffffu;
+  if (i0 < 0) return (words[0] << -i0) | ((1u << -i0) - 1u);
+  const int w = i0 >> 5, k = i0 & 31;
+  const uint32_t lo = w < W ? words[w] : 0u;
+  if (k == 0) return lo;
+  const uint32_t hi = w + 1 < W ? words[w + 1] : 0u;
+  return (lo >> k) | (hi << (32 - k));
+}
+
+template <int D, bool kE4M3, int NT, int WQ>
+struct AttnShape {
+  static constexpr int WT = kAttnWaves / WQ;
+  static constexpr int TK = (WT == 4 || D == 64) ? 128 : 64;  // tokens per tile
+  static constexpr int M = 16 * NT * WQ;                      // rows per workgroup
+  static constexpr int kTileBytes = 2 * TK * D * 2;
+  static constexpr int kJoinBytes = WT > 1 ? WT * M * (D + 4) * 4 : 0;
+  static constexpr int kLdsBytes = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
+};
+
+template <int D, bool kE4M3, int NT, int WQ>
+__global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv, AttnArgs a) {
+  using Shape = AttnShape<D, kE4M3, NT, WQ>;
+  constexpr int WT = Shape::WT, TK = Shape::TK, M = Shape::M;
+  constexpr int DT = D / 16, ST = D / 32;
+  constexpr int KB = D / 8;               // 16-byte blocks of a key row in LDS
+  constexpr int VB = TK / 8;              // 16-byte blocks of a row of V^T in LDS
+  constexpr int TW = TK / WT;             // tokens of a wave
+  constexpr int G = TW >= 64 ? 64 : 32;   // tokens per softmax step
+  constexpr int KE = kE4M3 ? 16 : 8;      // key elements per 16-byte load
+  constexpr int KL = TK * D / KE / kAttnBlock;        // key loads per thread
+  constexpr int VQ = TK * D / 32 / kAttnBlock;        // 4-token x 8-element value pieces
+  static_assert(KL >= 1 && VQ >= 1, "");
+  __shared__ __align__(16) unsigned char lds[Shape::kLdsBytes];
+  __shared__ float lds_ms[WT][M][2];
+  __shared__ int64_t lds_row[TK];         // cache rows of a tile that holds nodes
+  __shared__ int lds_odd;
+  vec16 *const lk = reinterpret_cast<vec16 *>(lds);
+  unsigned char *const lv = lds + TK * D * 2;
+
   // units on neighbouring blocks run on different XCDs; the row tiles of one
   // unit, which read the same keys and values, stay on one
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
@@ -299,121 +154,372 @@ __global__ __launch_bounds__(kAttnBlock) void kr_tree_attention(CacheView cv, At
   const int rows = (bad ? a.T : nodes) * a.group;
   if (mt * M >= rows) return;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wq = wave % WQ, wt = wave / WQ;
+  const float nan = __uint_as_float(0x7fc00000u);
+  const int total = bad ? 0 : ctx + nodes;
+  const int all_tiles = (total + TK - 1) / TK;
+  const int per = (all_tiles + a.S - 1) / a.S;
+  const int t_lo = s * per, t_hi = min(t_lo + per, all_tiles);
+
+  // the page of 16-token block `lane` of a tile, -1 for a bad one
+  const int32_t *table = a.table + b * cv.max_pages;
+  auto load_pages = [&](int tile) -> int {
+    const int64_t p = (int64_t)tile * TK + 16 * (lane % (TK / 16));
+    if (tile >= t_hi || p >= total) return -1;
+    const int pg = table[p >> cv.page_shift];
+    return pg >= 0 && pg < cv.n_pages ? pg : -1;
+  };
+  const int in_page = (1 << cv.page_shift) - 1;
+  auto row_of = [&](int pg, int64_t p) -> int64_t {  // cache row, or -1
+    return pg < 0 ? -1 : (((int64_t)pg * cv.Hkv + h) << cv.page_shift) + (p & in_page);
+  };
+
+  vec16 kreg[KL];
+  u32x4 vreg[VQ][kE4M3 ? 2 : 4];
+  int ksc[KL], kok = 0, vok = 0;
+  uint32_t vsc[VQ];
+  // this thread's share of a tile: keys by 16 bytes, values by 4 tokens x 8 elements
+  auto load_tile = [&](int tile, int pages) {
+    const int64_t p0 = (int64_t)tile * TK;
+    kok = vok = 0;
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      const int tok = tid / (D / KE) + j * (kAttnBlock / (D / KE)), ch = tid % (D / KE);
+      const int64_t row = row_of(__shfl(pages, tok / 16, 64), p0 + tok);
+      if (row >= 0) {
+        kok |= 1 << j;
+        kreg[j] = *reinterpret_cast<const vec16 *>(cv.k + (row * D + ch * KE) * (kE4M3 ? 1 : 2));
+        if constexpr (kE4M3) ksc[j] = cv.k_scale[row];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VQ; ++j) {
+      const int q = tid / (D / 8) + j * (kAttnBlock / (D / 8)), ch = tid % (D / 8);
+      const int64_t row = row_of(__shfl(pages, q / 4, 64), p0 + 4 * q);  // 4 tokens, one page
+      if (row >= 0) {
+        vok |= 1 << j;
+        if constexpr (kE4M3) {
+          vsc[j] = *reinterpret_cast<const uint32_t *>(cv.v_scale + row);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const u32x2 x = *reinterpret_cast<const u32x2 *>(cv.v + (row + 2 * i) * D + ch * 8);
+            const u32x2 y = *reinterpret_cast<const u32x2 *>(cv.v + (row + 2 * i + 1) * D + ch * 8);
+            vreg[j][i] = u32x4{x.x, x.y, y.x, y.y};
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            vreg[j][i] = *reinterpret_cast<const vec16 *>(cv.v + ((row + i) * D + ch * 8) * 2);
+        }
+      }
+    }
+  };
+  // registers to LDS.  A token without a valid page gets NaN keys, so that every row
+  // that attends to it is NaN; values behind the end are zero.
+  auto store_tile = [&](int tile, bool last, int pages) {
+    const int left = min((int64_t)TK, total - (int64_t)tile * TK);
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      const int tok = tid / (D / KE) + j * (kAttnBlock / (D / KE)), ch = tid % (D / KE);
+      vec16 w[KE / 8];
+      if (!((kok >> j) & 1)) {
+#pragma unroll
+        for (int i = 0; i < KE / 8; ++i) w[i] = vec16{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+      } else if constexpr (kE4M3) {
+        const float sc = pow2_of_scale(ksc[j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = i ? kreg[j].z : kreg[j].x, y = i ? kreg[j].w : kreg[j].y;
+          w[i] = vec16{widen2<false>(x, sc), widen2<true>(x, sc), widen2<false>(y, sc),
+                       widen2<true>(y, sc)};
+        }
+      } else {
+        w[0] = kreg[j];
+      }
+#pragma unroll
+      for (int i = 0; i < KE / 8; ++i)
+        lk[tok * KB + ((ch * (KE / 8) + i) ^ (tok & (KB - 1)))] = w[i];
+    }
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < VQ; ++j) {
+      const int q = tid / (D / 8) + j * (kAttnBlock / (D / 8)), ch = tid % (D / 8);
+      uint32_t x[4][4];  // token, pair of neighbouring elements
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kE4M3) {
+          const float sc = pow2_of_scale((vsc[j] >> (8 * i)) & 255);
+          const uint32_t u = vreg[j][i / 2][2 * (i & 1)], v = vreg[j][i / 2][2 * (i & 1) + 1];
+          x[i][0] = widen2<false>(u, sc);
+          x[i][1] = widen2<true>(u, sc);
+          x[i][2] = widen2<false>(v, sc);
+          x[i][3] = widen2<true>(v, sc);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = vreg[j][i][e];
+        }
+      }
+      if (last) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool there = 4 * q + i < left && ((vok >> j) & 1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!there) x[i][e] = 0;
+            // 0 * NaN is NaN: values that are not finite stay out of the product
+            // and join the rows that attend to them one by one
+            if ((x[i][e] & 0x7f80u) == 0x7f80u) {
+              odd = true;
+              x[i][e] &= 0xffff0000u;
+            }
+            if ((x[i][e] & 0x7f800000u) == 0x7f800000u) {
+              odd = true;
+              x[i][e] &= 0x0000ffffu;
+            }
+          }
+        }
+      }
+      // tokens 4 g .. 4 g + 3 and 16 + 4 g .. of a group of 32 side by side: the
+      // order in which the first product leaves p
+      const int blk = (q / 8) * 4 + (q & 3), half = (q >> 2) & 1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = ch * 8 + e;
+        const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
+        const u32x2 w = {__builtin_amdgcn_perm(x[1][e / 2], x[0][e / 2], sel),
+                         __builtin_amdgcn_perm(x[3][e / 2], x[2][e / 2], sel)};
+        *reinterpret_cast<u32x2 *>(lv + d * (TK * 2) + ((blk ^ ((d / DT) & (VB - 1))) << 4) +
+                                   half * 8) = w;
+      }
+    }
+    if (last) {
+      if (odd) lds_odd = 1;
+      const int64_t row = row_of(__shfl(pages, (tid % TK) / 16, 64), (int64_t)tile * TK + tid % TK);
+      if (tid < TK) lds_row[tid] = tid < left ? row : -1;
+    }
+  };
 
   vec16 qf[NT][ST];
   int node[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = mt * M + 16 * t + n;
-    node[t] = min(r, rows - 1) / a.group;
+    const int r = min(mt * M + (wq * NT + t) * 16 + n, rows - 1);
+    node[t] = r / a.group;
     const uint16_t *q = a.q + (b * a.T + node[t]) * a.q_stride +
-                        (int64_t)(h * a.group + min(r, rows - 1) % a.group) * D;
+                        (int64_t)(h * a.group + r % a.group) * D;
 #pragma unroll
-    for (int i = 0; i < ST; ++i)
-      qf[t][i] = *reinterpret_cast<const vec16 *>(
-          q + (kE4M3 ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g));
+    for (int i = 0; i < ST; ++i) qf[t][i] = *reinterpret_cast<const vec16 *>(q + 32 * i + 8 * g);
   }
-  AttnState<D, NT> st;
+  // rows of this wave that exist
+  const bool active = mt * M + wq * NT * 16 < rows;
+  f32x4 o[NT][DT];
+  float m[NT], base[NT], l[NT];  // base = m * c as rounded: the exponent that l and o are held over
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    st.m[t] = kNegInf;
-    st.base[t] = kNegInf;
-    st.l[t] = 0.0f;
+    m[t] = base[t] = kNegInf;
+    l[t] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < DT; ++i) st.o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int W = (a.T + 31) / 32;
+
+  int pages = load_pages(t_lo), pages_next = load_pages(t_lo + 1);
+  if (t_lo < t_hi) load_tile(t_lo, pages);
+  for (int tile = t_lo; tile < t_hi; ++tile) {
+    const int64_t p0 = (int64_t)tile * TK;
+    const bool last = p0 + TK > ctx;  // holds nodes or the end
+    if (last) {
+      if (tid == 0) lds_odd = 0;
+      __syncthreads();
+    }
+    store_tile(tile, last, pages);
+    __syncthreads();
+    pages = pages_next;
+    if (tile + 1 < t_hi) load_tile(tile + 1, pages);
+    pages_next = load_pages(tile + 2);
+    if (active) {
+#pragma unroll
+      for (int g0 = 0; g0 < TW; g0 += G) {
+        const int k0 = wt * TW + g0;  // first token of the step within the tile
+        f32x4 sc[NT][G / 16];
+#pragma unroll
+        for (int u = 0; u < G / 16; ++u) {
+          const int tok = k0 + 16 * u + n;
+          vec16 kf[ST];
+#pragma unroll
+          for (int i = 0; i < ST; ++i) kf[i] = lk[tok * KB + ((4 * i + g) ^ (tok & (KB - 1)))];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            sc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < ST; ++i) sc[t][u] = mfma_bf16(kf[i], qf[t][i], sc[t][u]);
+          }
+        }
+        uint32_t allow[NT][G / 32];
+        if (last) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int w = 0; w < G / 32; ++w) {
+              const int64_t p = p0 + k0 + 32 * w;
+              const int64_t left = total - p;
+              uint32_t ok = left <= 0 ? 0u : left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+              ok &= allow_window(a.anc ? a.anc + (b * a.T + node[t]) * W : nullptr, W, node[t],
+                                 (int)(p - ctx));
+              allow[t][w] = ok;
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (!((ok >> (16 * u + 4 * g + r)) & 1u)) sc[t][2 * w + u][r] = kNegInf;
+            }
+        }
+        vec16 pf[NT][G / 32];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float mx = m[t];
+#pragma unroll
+          for (int u = 0; u < G / 16; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[t][u][r]);
+          mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+          mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+          if (__any(mx != m[t])) {
+            const float next = mx * a.c;
+            const float f = mx == m[t] ? 1.0f : fast_exp2(base[t] - next);
+            l[t] *= f;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[t][i] *= f;
+            m[t] = mx;
+            base[t] = next;
+          }
+          const float sub = mx == kNegInf ? 0.0f : base[t];
+#pragma unroll
+          for (int u = 0; u < G / 16; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              sc[t][u][r] = fast_exp2(__builtin_fmaf(sc[t][u][r], a.c, -sub));
+              l[t] += sc[t][u][r];
+            }
+#pragma unroll
+          for (int w = 0; w < G / 32; ++w)
+            pf[t][w] = vec16{pack_bf16(sc[t][2 * w][0], sc[t][2 * w][1]),
+                             pack_bf16(sc[t][2 * w][2], sc[t][2 * w][3]),
+                             pack_bf16(sc[t][2 * w + 1][0], sc[t][2 * w + 1][1]),
+                             pack_bf16(sc[t][2 * w + 1][2], sc[t][2 * w + 1][3])};
+        }
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w) {
+          const int blk = (k0 / 32 + w) * 4 + g;
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+            const int d = DT * n + i;
+            const vec16 vf = *reinterpret_cast<const vec16 *>(
+                lv + d * (TK * 2) + ((blk ^ (n & (VB - 1))) << 4));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[t][i] = mfma_bf16(vf, pf[t][w], o[t][i]);
+          }
+        }
+        if (last && lds_odd) {
+#pragma unroll
+          for (int u = 0; u < G / 16; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              for (int from = 0; from < 4; ++from) {
+                const int tok = 16 * u + 4 * from + r;
+                const int64_t row = lds_row[k0 + tok];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  const float pt = __shfl(sc[t][u][r], 16 * from + n, 64);
+                  if (row < 0 || !((allow[t][u / 2] >> (tok & 31)) & 1u)) continue;
+                  const float vs = kE4M3 ? pow2_of_scale(cv.v_scale[row]) : 1.0f;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < DT; ++i) {
+                      const int64_t at = row * D + DT * (4 * g + e) + i;
+                      float x;
+                      if constexpr (kE4M3)
+                        x = __builtin_amdgcn_cvt_f32_fp8((uint32_t)cv.v[at], 0) * vs;
+                      else
+                        x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(cv.v)[at]
+                                            << 16);
+                      if (!(fabsf(x) < __builtin_huge_valf())) o[t][i][e] += pt * x;
+                    }
+                }
+              }
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+    if (bad) l[t] = nan;
   }
 
-  if (!bad) {
-    const int ctx_tiles = (ctx + kAttnTile - 1) / kAttnTile;
-    const int tree_tiles = (nodes + kAttnTile - 1) / kAttnTile;
-    const int all_tiles = ctx_tiles + tree_tiles;
-    const int per = (all_tiles + a.S - 1) / a.S;
-    const int lo = s * per, hi = min(lo + per, all_tiles);
-    const int W = (a.T + 31) / 32;
-    for (int tile = lo + wave; tile < hi; tile += kAttnWaves) {
-      const bool tree = tile >= ctx_tiles;
-      const int64_t p0 = tree ? (int64_t)ctx + (int64_t)(tile - ctx_tiles) * kAttnTile
-                              : (int64_t)tile * kAttnTile;
-      const int left = (int)min((int64_t)kAttnTile, (tree ? (int64_t)ctx + nodes : ctx) - p0);
-      int64_t row_k[2], row_v[8];
-      bool poison = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = 16 * i + n;
-        row_k[i] = k < left ? cache_row(cv, b, p0 + k, h) : -1;
-        poison |= k < left && row_k[i] < 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = 16 * (i >> 2) + 4 * g + (i & 3);
-        row_v[i] = k < left ? cache_row(cv, b, p0 + k, h) : -1;
-      }
-      poison = __any(poison);
-      const uint32_t there = left == 32 ? 0xffffffffu : (1u << left) - 1u;
-      uint32_t allow[NT];
-      if (tree) {
-        const int w = tile - ctx_tiles;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          allow[t] = there & (a.anc ? a.anc[(b * a.T + node[t]) * W + w]
-                                    : range_bits(0, node[t], w));
-        attn_tile<D, kE4M3, NT, true>(cv, qf, row_k, row_v, allow, false, poison, a.c, st);
-      } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) allow[t] = there;
-        attn_tile<D, kE4M3, NT, false>(cv, qf, row_k, row_v, allow, left == 32, poison, a.c, st);
-      }
-    }
-  }
-  // join the waves: O over the largest maximum, l summed over the lanes of a row
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    st.l[t] += __shfl_xor(st.l[t], 16, 64);
-    st.l[t] += __shfl_xor(st.l[t], 32, 64);
-    if (g == 0) {
-      lds_ms[wave][16 * t + n][0] = st.base[t];
-      lds_ms[wave][16 * t + n][1] = st.l[t];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int i = 0; i < DT; i += 4)
-        *reinterpret_cast<f32x4 *>(&lds_o[wave][16 * t + n][DT * (4 * g + r) + i]) =
-            f32x4{st.o[t][i][r], st.o[t][i + 1][r], st.o[t][i + 2][r], st.o[t][i + 3][r]};
-  }
-  __syncthreads();
-  constexpr int V = D / 4;  // 16-byte pieces of a row
-  for (int i = tid; i < M * V; i += kAttnBlock) {
-    const int r = i / V, d = (i % V) * 4;
-    if (mt * M + r >= rows) continue;
-    float m = kNegInf, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) m = fmaxf(m, lds_ms[w][r][0]);
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      const float f = part_factor(lds_ms[w][r][0], lds_ms[w][r][1], m);
-      l += lds_ms[w][r][1] * f;
-      o += *reinterpret_cast<const f32x4 *>(&lds_o[w][r][d]) * f;
-    }
-    if (bad) l = __uint_as_float(0x7fc00000u);
-    const int R = mt * M + r;
+  // one row's 4 elements from d on, its exponent and its sum
+  auto put = [&](int R, int d, f32x4 x, float mm, float ll, bool first) {
     const int64_t row = (b * a.T + R / a.group) * Hq + h * a.group + R % a.group;
     if (a.S > 1) {
       const int64_t pr = (int64_t)s * a.rows_all + row;
-      *reinterpret_cast<f32x4 *>(a.part_o + pr * D + d) = o;
-      if (d == 0) {
-        a.part_ms[2 * pr] = m;
-        a.part_ms[2 * pr + 1] = l;
+      *reinterpret_cast<f32x4 *>(a.part_o + pr * D + d) = x;
+      if (first) {
+        a.part_ms[2 * pr] = mm;
+        a.part_ms[2 * pr + 1] = ll;
       }
     } else {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      uint2 w;
-      w.x = pack_bf16(o[0] * inv, o[1] * inv);
-      w.y = pack_bf16(o[2] * inv, o[3] * inv);
-      *reinterpret_cast<uint2 *>(a.out + row * D + d) = w;
-      if (d == 0 && a.lse)
-        a.lse[row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.6931471805599453f;
+      attn_row_out<D>(a, row, d, x, mm, ll, first);
+    }
+  };
+  if constexpr (WT == 1) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int R = mt * M + (wq * NT + t) * 16 + n;
+      if (R >= rows) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < DT; i += 4)
+          put(R, DT * (4 * g + r) + i,
+              f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]}, base[t], l[t],
+              g == 0 && r == 0 && i == 0);
+    }
+  } else {
+    // the waves that split the tokens join over the largest exponent
+    float (*lo)[M][D + 4] = reinterpret_cast<float (*)[M][D + 4]>(lds);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int R = (wq * NT + t) * 16 + n;
+      if (g == 0) {
+        lds_ms[wt][R][0] = base[t];
+        lds_ms[wt][R][1] = l[t];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < DT; i += 4)
+          *reinterpret_cast<f32x4 *>(&lo[wt][R][DT * (4 * g + r) + i]) =
+              f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]};
+    }
+    __syncthreads();
+    constexpr int V = D / 4;  // 16-byte pieces of a row
+    for (int i = tid; i < M * V; i += kAttnBlock) {
+      const int r = i / V, d = (i % V) * 4;
+      if (mt * M + r >= rows) break;
+      float mm = kNegInf, ll = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WT; ++w) mm = fmaxf(mm, lds_ms[w][r][0]);
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < WT; ++w) {
+        const float f = part_factor(lds_ms[w][r][0], lds_ms[w][r][1], mm);
+        ll += lds_ms[w][r][1] * f;
+        x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
+      }
+      put(mt * M + r, d, x, mm, ll, d == 0);
     }
   }
 }
@@ -441,13 +547,7 @@ __global__ __launch_bounds__(kAttnBlock) void kr_attn_join(AttnArgs a, int Hq) {
     l += ls * f;
     o += *reinterpret_cast<const f32x4 *>(a.part_o + pr * D + d) * f;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint2 w;
-  w.x = pack_bf16(o[0] * inv, o[1] * inv);
-  w.y = pack_bf16(o[2] * inv, o[3] * inv);
-  *reinterpret_cast<uint2 *>(a.out + row * D + d) = w;
-  if (d == 0 && a.lse)
-    a.lse[row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.6931471805599453f;
+  attn_row_out<D>(a, row, d, o, m, l, d == 0);
 }
 
 }  // namespace svd

@@ -86,22 +86,23 @@ int read_kind(bool e4m3, int D, const CacheView &c, const int32_t *start, const 
                  : read_rows<E, false, 128>(c, start, count, B, N, k, v, s);
 }
 
-// Rows per wave and parts of an attention call: a function of the sizes alone.
+// Rows per workgroup and parts of an attention call: a function of the sizes alone.
 struct AttnPlan {
-  int nt, m_tiles, S;
+  int nt, wq, m_tiles, S;
 };
 
 constexpr int64_t kAttnTargetGroups = 1024;  // workgroups to aim for: four per CU
-constexpr int kAttnPartTiles = 8;            // a part walks at least this many tiles
+constexpr int kAttnPartTokens = 256;         // a part walks at least this many tokens
 
 AttnPlan attn_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int64_t room) {
   AttnPlan p;
   const int64_t rows = (int64_t)T * (Hq / Hkv);
-  p.nt = rows <= 16 ? 1 : 2;
-  p.m_tiles = (int)((rows + 16 * p.nt - 1) / (16 * p.nt));
+  p.nt = rows <= 64 ? 1 : 2;
+  p.wq = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const int m = 16 * p.nt * p.wq;
+  p.m_tiles = (int)((rows + m - 1) / m);
   const int64_t base = B * Hkv * p.m_tiles;
-  const int64_t tiles = (room + kAttnTile - 1) / kAttnTile + 1;
-  const int64_t most = std::max<int64_t>(1, tiles / kAttnPartTiles);
+  const int64_t most = std::max<int64_t>(1, room / kAttnPartTokens);
   const int64_t want = (kAttnTargetGroups + base - 1) / base;
   p.S = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, kAttnMaxSplits}));
   return p;
@@ -121,11 +122,11 @@ size_t attn_ms_offset(int64_t rows, int S, int D) {
   return align_up((size_t)rows * S * D * sizeof(float));
 }
 
-template <int D, bool kE4M3, int NT>
+template <int D, bool kE4M3, int NT, int WQ>
 int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   CallTimer tm;
   const int64_t grid = ((int64_t)a.units + 7) / 8 * 8 * a.m_tiles;
-  SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT>,
+  SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ>,
              dim3((unsigned)grid), dim3(kAttnBlock), s, c, a);
   if (a.S > 1) {
     constexpr int rows = kAttnBlock / (D / 4);
@@ -136,9 +137,11 @@ int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
 }
 
 template <int D, bool kE4M3>
-int attn_rows(int nt, const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
-  if (nt == 1) return attn_launch<D, kE4M3, 1>(c, a, Hq, s);
-  return attn_launch<D, kE4M3, 2>(c, a, Hq, s);
+int attn_rows(const AttnPlan &p, const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
+  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4>(c, a, Hq, s);
+  if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4>(c, a, Hq, s);
+  if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2>(c, a, Hq, s);
+  return attn_launch<D, kE4M3, 1, 1>(c, a, Hq, s);
 }
 
 template <typename E, bool kVec, bool kBias, int PATH>
@@ -261,6 +264,7 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
   a.q_stride = q_stride;
   a.ctx_len = ctx_len;
   a.n_nodes = n_nodes;
+  a.table = c.table;
   a.anc = anc;
   a.room = room;
   a.T = T;
@@ -277,10 +281,10 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
                                         attn_ms_offset(a.rows_all, p.S, D));
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (cache->dtype == SVD_CACHE_E4M3)
-    return D == 64 ? attn_rows<64, true>(p.nt, c, a, q_heads, s)
-                   : attn_rows<128, true>(p.nt, c, a, q_heads, s);
-  return D == 64 ? attn_rows<64, false>(p.nt, c, a, q_heads, s)
-                 : attn_rows<128, false>(p.nt, c, a, q_heads, s);
+    return D == 64 ? attn_rows<64, true>(p, c, a, q_heads, s)
+                   : attn_rows<128, true>(p, c, a, q_heads, s);
+  return D == 64 ? attn_rows<64, false>(p, c, a, q_heads, s)
+                 : attn_rows<128, false>(p, c, a, q_heads, s);
 }
 
 int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t B, int32_t T,
