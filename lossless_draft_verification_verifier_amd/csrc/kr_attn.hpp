@@ -79,6 +79,16 @@ __device__ __forceinline__ bool attn_bad(int ctx, int nodes, int T, int64_t room
   return ctx < 0 || nodes < 0 || nodes > T || (int64_t)ctx + nodes > room;
 }
 
+// one element of a cached row
+template <bool kE4M3, int D>
+__device__ __forceinline__ float cache_element(const uint8_t *p, const uint8_t *scale, int64_t row,
+                                               int d) {
+  if constexpr (kE4M3)
+    return __builtin_amdgcn_cvt_f32_fp8((uint32_t)p[row * D + d], 0) * pow2_of_scale(scale[row]);
+  else
+    return BF16::at(reinterpret_cast<const uint16_t *>(p) + row * D, d);
+}
+
 // 4 elements of an output row: o over its sum, and the row's log-sum.
 template <int D>
 __device__ __forceinline__ void attn_row_out(const AttnArgs &a, int64_t row, int d, f32x4 o, float m,
@@ -114,7 +124,7 @@ struct AttnShape {
   static constexpr int TK = (WT == 4 || D == 64) ? 128 : 64;  // tokens per tile
   static constexpr int M = 16 * NT * WQ;                      // rows per workgroup
   static constexpr int kTileBytes = 2 * TK * D * 2;
-  static constexpr int kJoinBytes = WT > 1 ? WT * M * (D + 4) * 4 : 0;
+  static constexpr int kJoinBytes = WT * 16 * WQ * (D + 4) * 4;
   static constexpr int kLdsBytes = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
 };
 
@@ -132,9 +142,8 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
   constexpr int VQ = TK * D / 32 / kAttnBlock;        // 4-token x 8-element value pieces
   static_assert(KL >= 1 && VQ >= 1, "");
   __shared__ __align__(16) unsigned char lds[Shape::kLdsBytes];
-  __shared__ float lds_ms[WT][M][2];
-  __shared__ int64_t lds_row[TK];         // cache rows of a tile that holds nodes
-  __shared__ int lds_odd;
+  __shared__ float lds_ms[WT][16 * WQ][2];
+  __shared__ int lds_odd;                 // some node of this part has a value that is not finite
   vec16 *const lk = reinterpret_cast<vec16 *>(lds);
   unsigned char *const lv = lds + TK * D * 2;
 
@@ -216,7 +225,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
   };
   // registers to LDS.  A token without a valid page gets NaN keys, so that every row
   // that attends to it is NaN; values behind the end are zero.
-  auto store_tile = [&](int tile, bool last, int pages) {
+  auto store_tile = [&](int tile, bool last) {
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
@@ -267,7 +276,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
           for (int e = 0; e < 4; ++e) {
             if (!there) x[i][e] = 0;
             // 0 * NaN is NaN: values that are not finite stay out of the product
-            // and join the rows that attend to them one by one
+            // and join the rows that attend to them at the end
             if ((x[i][e] & 0x7f80u) == 0x7f80u) {
               odd = true;
               x[i][e] &= 0xffff0000u;
@@ -292,11 +301,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
                                    half * 8) = w;
       }
     }
-    if (last) {
-      if (odd) lds_odd = 1;
-      const int64_t row = row_of(__shfl(pages, (tid % TK) / 16, 64), (int64_t)tile * TK + tid % TK);
-      if (tid < TK) lds_row[tid] = tid < left ? row : -1;
-    }
+    if (odd) lds_odd = 1;
   };
 
   vec16 qf[NT][ST];
@@ -323,16 +328,14 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
   }
   const int W = (a.T + 31) / 32;
 
+  if (tid == 0) lds_odd = 0;
+  __syncthreads();
   int pages = load_pages(t_lo), pages_next = load_pages(t_lo + 1);
   if (t_lo < t_hi) load_tile(t_lo, pages);
   for (int tile = t_lo; tile < t_hi; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
     const bool last = p0 + TK > ctx;  // holds nodes or the end
-    if (last) {
-      if (tid == 0) lds_odd = 0;
-      __syncthreads();
-    }
-    store_tile(tile, last, pages);
+    store_tile(tile, last);
     __syncthreads();
     pages = pages_next;
     if (tile + 1 < t_hi) load_tile(tile + 1, pages);
@@ -355,7 +358,6 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
             for (int i = 0; i < ST; ++i) sc[t][u] = mfma_bf16(kf[i], qf[t][i], sc[t][u]);
           }
         }
-        uint32_t allow[NT][G / 32];
         if (last) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -366,7 +368,6 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
               uint32_t ok = left <= 0 ? 0u : left >= 32 ? 0xffffffffu : (1u << left) - 1u;
               ok &= allow_window(a.anc ? a.anc + (b * a.T + node[t]) * W : nullptr, W, node[t],
                                  (int)(p - ctx));
-              allow[t][w] = ok;
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -420,35 +421,6 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
             for (int t = 0; t < NT; ++t) o[t][i] = mfma_bf16(vf, pf[t][w], o[t][i]);
           }
         }
-        if (last && lds_odd) {
-#pragma unroll
-          for (int u = 0; u < G / 16; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              for (int from = 0; from < 4; ++from) {
-                const int tok = 16 * u + 4 * from + r;
-                const int64_t row = lds_row[k0 + tok];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                  const float pt = __shfl(sc[t][u][r], 16 * from + n, 64);
-                  if (row < 0 || !((allow[t][u / 2] >> (tok & 31)) & 1u)) continue;
-                  const float vs = kE4M3 ? pow2_of_scale(cv.v_scale[row]) : 1.0f;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                      const int64_t at = row * D + DT * (4 * g + e) + i;
-                      float x;
-                      if constexpr (kE4M3)
-                        x = __builtin_amdgcn_cvt_f32_fp8((uint32_t)cv.v[at], 0) * vs;
-                      else
-                        x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(cv.v)[at]
-                                            << 16);
-                      if (!(fabsf(x) < __builtin_huge_valf())) o[t][i][e] += pt * x;
-                    }
-                }
-              }
-        }
       }
     }
     __syncthreads();
@@ -474,41 +446,57 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
       attn_row_out<D>(a, row, d, x, mm, ll, first);
     }
   };
-  if constexpr (WT == 1) {
+  // what the nodes of this part with values that are not finite add to 4 elements
+  auto odd_values = [&](int R, int d, f32x4 x, float mm) {
+    const int nd = R / a.group;
+    const uint16_t *q = a.q + (b * a.T + nd) * a.q_stride +
+                        (int64_t)(h * a.group + R % a.group) * D;
+    const int64_t lo = max((int64_t)t_lo * TK, (int64_t)ctx);
+    const int64_t hi = min((int64_t)t_hi * TK, (int64_t)total);
+    for (int64_t p = lo; p < hi; ++p) {
+      const int i = (int)(p - ctx);
+      if (a.anc ? !((a.anc[(b * a.T + nd) * W + (i >> 5)] >> (i & 31)) & 1u) : i > nd) continue;
+      const int64_t row = cache_row(cv, b, p, h);
+      if (row < 0) continue;
+      float v[4];
+      bool odd = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int R = mt * M + (wq * NT + t) * 16 + n;
-      if (R >= rows) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < DT; i += 4)
-          put(R, DT * (4 * g + r) + i,
-              f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]}, base[t], l[t],
-              g == 0 && r == 0 && i == 0);
-    }
-  } else {
-    // the waves that split the tokens join over the largest exponent
-    float (*lo)[M][D + 4] = reinterpret_cast<float (*)[M][D + 4]>(lds);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int R = (wq * NT + t) * 16 + n;
-      if (g == 0) {
-        lds_ms[wt][R][0] = base[t];
-        lds_ms[wt][R][1] = l[t];
+      for (int e = 0; e < 4; ++e) {
+        v[e] = cache_element<kE4M3, D>(cv.v, cv.v_scale, row, d + e);
+        odd |= !(fabsf(v[e]) < __builtin_huge_valf());
       }
+      if (!odd) continue;
+      float z = 0.0f;
+      for (int e = 0; e < D; ++e)
+        z += cache_element<kE4M3, D>(cv.k, cv.k_scale, row, e) * BF16::at(q, e);
+      const float pt = fast_exp2(__builtin_fmaf(z, a.c, -(mm == kNegInf ? 0.0f : mm)));
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < DT; i += 4)
-          *reinterpret_cast<f32x4 *>(&lo[wt][R][DT * (4 * g + r) + i]) =
-              f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]};
+      for (int e = 0; e < 4; ++e)
+        if (!(fabsf(v[e]) < __builtin_huge_valf())) x[e] += pt * v[e];
     }
+    return x;
+  };
+  // the waves that split the tokens join over the largest exponent, 16 * WQ rows at a time
+  float (*lo)[16 * WQ][D + 4] = reinterpret_cast<float (*)[16 * WQ][D + 4]>(lds);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (t > 0) __syncthreads();
+    if (g == 0) {
+      lds_ms[wt][wq * 16 + n][0] = base[t];
+      lds_ms[wt][wq * 16 + n][1] = l[t];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < DT; i += 4)
+        *reinterpret_cast<f32x4 *>(&lo[wt][wq * 16 + n][DT * (4 * g + r) + i]) =
+            f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]};
     __syncthreads();
     constexpr int V = D / 4;  // 16-byte pieces of a row
-    for (int i = tid; i < M * V; i += kAttnBlock) {
+    for (int i = tid; i < 16 * WQ * V; i += kAttnBlock) {
       const int r = i / V, d = (i % V) * 4;
-      if (mt * M + r >= rows) break;
+      const int R = mt * M + ((r >> 4) * NT + t) * 16 + (r & 15);
+      if (R >= rows) continue;
       float mm = kNegInf, ll = 0.0f;
 #pragma unroll
       for (int w = 0; w < WT; ++w) mm = fmaxf(mm, lds_ms[w][r][0]);
@@ -519,7 +507,8 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
         ll += lds_ms[w][r][1] * f;
         x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
       }
-      put(mt * M + r, d, x, mm, ll, d == 0);
+      if (lds_odd) x = odd_values(R, d, x, mm);
+      put(R, d, x, mm, ll, d == 0);
     }
   }
 }
