@@ -61,6 +61,10 @@ __device__ __forceinline__ f32x4 mfma_bf16(const vec16 &a, const vec16 &b, const
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+__device__ __forceinline__ float scale_factor(uint32_t byte) {  // of a byte from 1 to 254
+  return __uint_as_float(byte << 23);
+}
+
 // two E4M3 codes of word w, times the power of two s, as bf16
 template <bool kHigh>
 __device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
@@ -123,6 +127,7 @@ struct AttnShape {
   static constexpr int WT = kAttnWaves / WQ;
   static constexpr int TK = (WT == 4 || D == 64) ? 128 : 64;  // tokens per tile
   static constexpr int M = 16 * NT * WQ;                      // rows per workgroup
+  static constexpr int PF = 1;                                // tiles on their way at a time
   static constexpr int kTileBytes = 2 * TK * D * 2;
   static constexpr int kJoinBytes = WT * 16 * WQ * (D + 4) * 4;
   static constexpr int kLdsBytes = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
@@ -140,6 +145,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
   constexpr int KE = kE4M3 ? 16 : 8;      // key elements per 16-byte load
   constexpr int KL = TK * D / KE / kAttnBlock;        // key loads per thread
   constexpr int VQ = TK * D / 32 / kAttnBlock;        // 4-token x 8-element value pieces
+  constexpr int PF = Shape::PF;
   static_assert(KL >= 1 && VQ >= 1, "");
   __shared__ __align__(16) unsigned char lds[Shape::kLdsBytes];
   __shared__ float lds_ms[WT][16 * WQ][2];
@@ -183,22 +189,24 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
     return pg < 0 ? -1 : (((int64_t)pg * cv.Hkv + h) << cv.page_shift) + (p & in_page);
   };
 
-  vec16 kreg[KL];
-  u32x4 vreg[VQ][kE4M3 ? 2 : 4];
-  int ksc[KL], kok = 0, vok = 0;
-  uint32_t vsc[VQ];
+  struct Staged {  // a thread's share of a tile on its way to LDS
+    vec16 kreg[KL];
+    u32x4 vreg[VQ][kE4M3 ? 2 : 4];
+    int ksc[KL], kok, vok;
+    uint32_t vsc[VQ];
+  };
   // this thread's share of a tile: keys by 16 bytes, values by 4 tokens x 8 elements
-  auto load_tile = [&](int tile, int pages) {
+  auto load_tile = [&](Staged &st, int tile, int pages) {
     const int64_t p0 = (int64_t)tile * TK;
-    kok = vok = 0;
+    st.kok = st.vok = 0;
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       const int tok = tid / (D / KE) + j * (kAttnBlock / (D / KE)), ch = tid % (D / KE);
       const int64_t row = row_of(__shfl(pages, tok / 16, 64), p0 + tok);
       if (row >= 0) {
-        kok |= 1 << j;
-        kreg[j] = *reinterpret_cast<const vec16 *>(cv.k + (row * D + ch * KE) * (kE4M3 ? 1 : 2));
-        if constexpr (kE4M3) ksc[j] = cv.k_scale[row];
+        st.kok |= 1 << j;
+        st.kreg[j] = *reinterpret_cast<const vec16 *>(cv.k + (row * D + ch * KE) * (kE4M3 ? 1 : 2));
+        if constexpr (kE4M3) st.ksc[j] = cv.k_scale[row];
       }
     }
 #pragma unroll
@@ -206,44 +214,44 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
       const int q = tid / (D / 8) + j * (kAttnBlock / (D / 8)), ch = tid % (D / 8);
       const int64_t row = row_of(__shfl(pages, q / 4, 64), p0 + 4 * q);  // 4 tokens, one page
       if (row >= 0) {
-        vok |= 1 << j;
+        st.vok |= 1 << j;
         if constexpr (kE4M3) {
-          vsc[j] = *reinterpret_cast<const uint32_t *>(cv.v_scale + row);
+          st.vsc[j] = *reinterpret_cast<const uint32_t *>(cv.v_scale + row);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const u32x2 x = *reinterpret_cast<const u32x2 *>(cv.v + (row + 2 * i) * D + ch * 8);
             const u32x2 y = *reinterpret_cast<const u32x2 *>(cv.v + (row + 2 * i + 1) * D + ch * 8);
-            vreg[j][i] = u32x4{x.x, x.y, y.x, y.y};
+            st.vreg[j][i] = u32x4{x.x, x.y, y.x, y.y};
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            vreg[j][i] = *reinterpret_cast<const vec16 *>(cv.v + ((row + i) * D + ch * 8) * 2);
+            st.vreg[j][i] = *reinterpret_cast<const vec16 *>(cv.v + ((row + i) * D + ch * 8) * 2);
         }
       }
     }
   };
   // registers to LDS.  A token without a valid page gets NaN keys, so that every row
   // that attends to it is NaN; values behind the end are zero.
-  auto store_tile = [&](int tile, bool last) {
+  auto store_tile = [&](const Staged &st, int tile, bool last) {
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       const int tok = tid / (D / KE) + j * (kAttnBlock / (D / KE)), ch = tid % (D / KE);
       vec16 w[KE / 8];
-      if (!((kok >> j) & 1)) {
+      if (!((st.kok >> j) & 1)) {
 #pragma unroll
         for (int i = 0; i < KE / 8; ++i) w[i] = vec16{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
       } else if constexpr (kE4M3) {
-        const float sc = pow2_of_scale(ksc[j]);
+        const float sc = scale_factor(st.ksc[j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t x = i ? kreg[j].z : kreg[j].x, y = i ? kreg[j].w : kreg[j].y;
+          const uint32_t x = i ? st.kreg[j].z : st.kreg[j].x, y = i ? st.kreg[j].w : st.kreg[j].y;
           w[i] = vec16{widen2<false>(x, sc), widen2<true>(x, sc), widen2<false>(y, sc),
                        widen2<true>(y, sc)};
         }
       } else {
-        w[0] = kreg[j];
+        w[0] = st.kreg[j];
       }
 #pragma unroll
       for (int i = 0; i < KE / 8; ++i)
@@ -257,21 +265,21 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (kE4M3) {
-          const float sc = pow2_of_scale((vsc[j] >> (8 * i)) & 255);
-          const uint32_t u = vreg[j][i / 2][2 * (i & 1)], v = vreg[j][i / 2][2 * (i & 1) + 1];
+          const float sc = scale_factor((st.vsc[j] >> (8 * i)) & 255);
+          const uint32_t u = st.vreg[j][i / 2][2 * (i & 1)], v = st.vreg[j][i / 2][2 * (i & 1) + 1];
           x[i][0] = widen2<false>(u, sc);
           x[i][1] = widen2<true>(u, sc);
           x[i][2] = widen2<false>(v, sc);
           x[i][3] = widen2<true>(v, sc);
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] = vreg[j][i][e];
+          for (int e = 0; e < 4; ++e) x[i][e] = st.vreg[j][i][e];
         }
       }
       if (last) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool there = 4 * q + i < left && ((vok >> j) & 1);
+          const bool there = 4 * q + i < left && ((st.vok >> j) & 1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (!there) x[i][e] = 0;
@@ -318,10 +326,10 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
   // rows of this wave that exist
   const bool active = mt * M + wq * NT * 16 < rows;
   f32x4 o[NT][DT];
-  float m[NT], base[NT], l[NT];  // base = m * c as rounded: the exponent that l and o are held over
+  float base[NT], l[NT];  // base: the exponent that l and o are held over
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t] = base[t] = kNegInf;
+    base[t] = kNegInf;
     l[t] = 0.0f;
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -330,34 +338,42 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
 
   if (tid == 0) lds_odd = 0;
   __syncthreads();
-  int pages = load_pages(t_lo), pages_next = load_pages(t_lo + 1);
-  if (t_lo < t_hi) load_tile(t_lo, pages);
-  for (int tile = t_lo; tile < t_hi; ++tile) {
+  Staged st[PF];
+  int pages = load_pages(t_lo);
+#pragma unroll
+  for (int k = 0; k < PF; ++k) {
+    if (t_lo + k < t_hi) load_tile(st[k], t_lo + k, pages);
+    pages = load_pages(t_lo + k + 1);
+  }
+  for (int tile0 = t_lo; tile0 < t_hi; tile0 += PF)
+#pragma unroll
+  for (int k = 0; k < PF; ++k) {
+    const int tile = tile0 + k;
+    if (tile >= t_hi) break;
     const int64_t p0 = (int64_t)tile * TK;
     const bool last = p0 + TK > ctx;  // holds nodes or the end
-    store_tile(tile, last);
+    store_tile(st[k], tile, last);
     __syncthreads();
-    pages = pages_next;
-    if (tile + 1 < t_hi) load_tile(tile + 1, pages);
-    pages_next = load_pages(tile + 2);
+    if (tile + PF < t_hi) load_tile(st[k], tile + PF, pages);
+    pages = load_pages(tile + PF + 1);
     if (active) {
 #pragma unroll
       for (int g0 = 0; g0 < TW; g0 += G) {
         const int k0 = wt * TW + g0;  // first token of the step within the tile
         f32x4 sc[NT][G / 16];
 #pragma unroll
-        for (int u = 0; u < G / 16; ++u) {
-          const int tok = k0 + 16 * u + n;
-          vec16 kf[ST];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < ST; ++i) kf[i] = lk[tok * KB + ((4 * i + g) ^ (tok & (KB - 1)))];
+          for (int u = 0; u < G / 16; ++u) sc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            sc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < ST; ++i)
 #pragma unroll
-            for (int i = 0; i < ST; ++i) sc[t][u] = mfma_bf16(kf[i], qf[t][i], sc[t][u]);
+          for (int u = 0; u < G / 16; ++u) {
+            const int tok = k0 + 16 * u + n;
+            const vec16 kf = lk[tok * KB + ((4 * i + g) ^ (tok & (KB - 1)))];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][u] = mfma_bf16(kf, qf[t][i], sc[t][u]);
           }
-        }
         if (last) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -378,23 +394,25 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
         vec16 pf[NT][G / 32];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float mx = m[t];
+          float mx = kNegInf;
 #pragma unroll
           for (int u = 0; u < G / 16; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[t][u][r]);
           mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
           mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-          if (__any(mx != m[t])) {
-            const float next = mx * a.c;
-            const float f = mx == m[t] ? 1.0f : fast_exp2(base[t] - next);
+          // the exponent moves when a score passes it by 2^8: p, l and o lose nothing to
+          // a factor of at most 256, and most steps rescale nothing
+          const float next = mx * a.c;
+          const bool move = next > base[t] + 8.0f;
+          if (__any(move)) {
+            const float f = move ? fast_exp2(base[t] - next) : 1.0f;
             l[t] *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[t][i] *= f;
-            m[t] = mx;
-            base[t] = next;
+            base[t] = move ? next : base[t];
           }
-          const float sub = mx == kNegInf ? 0.0f : base[t];
+          const float sub = base[t] == kNegInf ? 0.0f : base[t];
 #pragma unroll
           for (int u = 0; u < G / 16; ++u)
 #pragma unroll

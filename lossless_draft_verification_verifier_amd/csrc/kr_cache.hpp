@@ -38,11 +38,11 @@ __device__ __forceinline__ int64_t cache_row(const CacheView &c, int64_t b, int6
   return ((pg * c.Hkv + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
-__device__ __forceinline__ uint16_t to_bf16(float x) {
-  return __builtin_bit_cast(uint16_t, (__bf16)x);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return (uint32_t)to_bf16(lo) | ((uint32_t)to_bf16(hi) << 16);
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // one instruction
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // The scale byte of a row whose largest finite magnitude is a: 448 = 1.75 * 2^8,
