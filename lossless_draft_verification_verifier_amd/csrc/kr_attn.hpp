@@ -11,14 +11,14 @@
 // per-lane factor, and the p that the first product leaves in a lane are the
 // operand the second one wants there, so p never crosses lanes.
 //
-// A workgroup of 4 waves takes 16 * NT * WQ rows and walks tiles of TK tokens:
-// every thread loads its share of the next tile into registers while the
-// current one is computed from LDS.  Writing the tile to LDS widens E4M3 rows to bf16
-// with their power of two (exact, by the conversion instruction) and transposes
-// V, once for all rows.  WQ waves split the rows; where there are few, WT =
-// 4 / WQ waves split the tile's tokens and merge at the end.  LDS rows hold 16-byte
-// blocks at an index xor'ed with the row, so that 16 lanes reading 16 rows
-// touch all banks.
+// A workgroup takes 16 * NT * WQ rows and walks tiles of TK tokens with two kinds
+// of waves.  4 waves keep the next PF tiles on their way in registers and write
+// one tile to LDS while the others compute the one before: widened from E4M3 to
+// bf16 with the row's power of two (exact, by the conversion instruction), and V
+// transposed, once for all rows.  WQ waves split the rows, and where these are few,
+// WT waves split the tile's tokens and merge at the end.  One barrier per tile.
+// LDS rows hold 16-byte blocks at an index xor'ed with the row, so that 16 lanes
+// reading 16 rows touch all banks.
 // p is rounded to bf16 once, as the operand of the second product; m, l and O
 // stay in 32 bits and l sums the unrounded p.
 //
@@ -37,8 +37,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef vec16 u32x4;
 
-constexpr int kAttnBlock = 256;
-constexpr int kAttnWaves = kAttnBlock / 64;
+constexpr int kAttnLoaders = 256;   // threads that bring tiles to LDS
+constexpr int kAttnJoinBlock = 256;
 constexpr int kAttnMaxSplits = 64;
 
 struct AttnArgs {
@@ -122,36 +122,37 @@ __device__ __forceinline__ uint32_t allow_window(const uint32_t *words, int W, i
   return (lo >> k) | (hi << (32 - k));
 }
 
-template <int D, bool kE4M3, int NT, int WQ>
+template <int D, bool kE4M3, int NT, int WQ, int WT>
 struct AttnShape {
-  static constexpr int WT = kAttnWaves / WQ;
-  static constexpr int TK = (WT == 4 || D == 64) ? 128 : 64;  // tokens per tile
-  static constexpr int M = 16 * NT * WQ;                      // rows per workgroup
-  static constexpr int PF = 1;                                // tiles on their way at a time
+  static constexpr int TK = 8192 / D;                 // tokens per tile: 32 KB of K and V
+  static constexpr int M = 16 * NT * WQ;              // rows per workgroup
+  static constexpr int NC = WQ * WT;                  // computing waves
+  static constexpr int kBlock = kAttnLoaders + 64 * NC;
+  static constexpr int PF = kE4M3 ? 3 : 2;            // tiles on their way at a time
+  static constexpr int kMinWaves = NT == 1 ? 4 : 2;   // per SIMD
   static constexpr int kTileBytes = 2 * TK * D * 2;
-  static constexpr int kJoinBytes = WT * 16 * WQ * (D + 4) * 4;
-  static constexpr int kLdsBytes = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
+  static constexpr int kJoinBytes = WT * M * (D + 4) * 4;
+  static constexpr int kLdsBytes = 2 * kTileBytes > kJoinBytes ? 2 * kTileBytes : kJoinBytes;
 };
 
-template <int D, bool kE4M3, int NT, int WQ>
-__global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv, AttnArgs a) {
-  using Shape = AttnShape<D, kE4M3, NT, WQ>;
-  constexpr int WT = Shape::WT, TK = Shape::TK, M = Shape::M;
+template <int D, bool kE4M3, int NT, int WQ, int WT>
+__global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
+                             (AttnShape<D, kE4M3, NT, WQ, WT>::kMinWaves))
+void kr_tree_attention(CacheView cv, AttnArgs a) {
+  using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
+  constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
   constexpr int DT = D / 16, ST = D / 32;
   constexpr int KB = D / 8;               // 16-byte blocks of a key row in LDS
   constexpr int VB = TK / 8;              // 16-byte blocks of a row of V^T in LDS
   constexpr int TW = TK / WT;             // tokens of a wave
-  constexpr int G = TW >= 64 ? 64 : 32;   // tokens per softmax step
+  constexpr int G = TW >= 64 && NT <= 2 ? 64 : 32;    // tokens per softmax step
   constexpr int KE = kE4M3 ? 16 : 8;      // key elements per 16-byte load
-  constexpr int KL = TK * D / KE / kAttnBlock;        // key loads per thread
-  constexpr int VQ = TK * D / 32 / kAttnBlock;        // 4-token x 8-element value pieces
-  constexpr int PF = Shape::PF;
-  static_assert(KL >= 1 && VQ >= 1, "");
+  constexpr int KL = TK * D / KE / kAttnLoaders;      // key loads per thread
+  // values: one piece of 4 tokens x 8 elements per thread
+  static_assert(KL >= 1 && TK * D == 32 * kAttnLoaders && TW % 32 == 0, "");
   __shared__ __align__(16) unsigned char lds[Shape::kLdsBytes];
-  __shared__ float lds_ms[WT][16 * WQ][2];
+  __shared__ float lds_ms[WT][M][2];
   __shared__ int lds_odd;                 // some node of this part has a value that is not finite
-  vec16 *const lk = reinterpret_cast<vec16 *>(lds);
-  unsigned char *const lv = lds + TK * D * 2;
 
   // units on neighbouring blocks run on different XCDs; the row tiles of one
   // unit, which read the same keys and values, stay on one
@@ -168,76 +169,89 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
   const bool bad = attn_bad(ctx, nodes, a.T, a.room);
   const int rows = (bad ? a.T : nodes) * a.group;
   if (mt * M >= rows) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int wq = wave % WQ, wt = wave / WQ;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int W = (a.T + 31) / 32;
   const float nan = __uint_as_float(0x7fc00000u);
   const int total = bad ? 0 : ctx + nodes;
   const int all_tiles = (total + TK - 1) / TK;
   const int per = (all_tiles + a.S - 1) / a.S;
   const int t_lo = s * per, t_hi = min(t_lo + per, all_tiles);
 
-  // the page of 16-token block `lane` of a tile, -1 for a bad one
+  if (threadIdx.x == 0) lds_odd = 0;
+  __syncthreads();
+
+  if (wave >= Shape::NC) {  // the waves that bring tiles to LDS
+  if (t_lo < t_hi) {
+  const int tid = threadIdx.x - 64 * Shape::NC;
+  // the table's entry for 16-token block `lane` of a tile.  It is looked at when the
+  // tile is loaded, not here: that would wait for it
   const int32_t *table = a.table + b * cv.max_pages;
+  const int blocks = (total + 15) / 16;
   auto load_pages = [&](int tile) -> int {
-    const int64_t p = (int64_t)tile * TK + 16 * (lane % (TK / 16));
-    if (tile >= t_hi || p >= total) return -1;
-    const int pg = table[p >> cv.page_shift];
-    return pg >= 0 && pg < cv.n_pages ? pg : -1;
+    const int blk = tile * (TK / 16) + lane % (TK / 16);
+    return table[min(blk, blocks - 1) >> (cv.page_shift - 4)];
   };
-  const int in_page = (1 << cv.page_shift) - 1;
-  auto row_of = [&](int pg, int64_t p) -> int64_t {  // cache row, or -1
-    return pg < 0 ? -1 : (((int64_t)pg * cv.Hkv + h) << cv.page_shift) + (p & in_page);
-  };
+  const uint32_t in_page = (1u << cv.page_shift) - 1;
+  constexpr uint32_t RB = kE4M3 ? D : 2 * D;  // bytes of a row
+  const uint32_t page_rows = (uint32_t)cv.Hkv << cv.page_shift, head_row = (uint32_t)h << cv.page_shift;
 
   struct Staged {  // a thread's share of a tile on its way to LDS
     vec16 kreg[KL];
-    u32x4 vreg[VQ][kE4M3 ? 2 : 4];
+    u32x4 vreg[kE4M3 ? 2 : 4];
     int ksc[KL], kok, vok;
-    uint32_t vsc[VQ];
+    uint32_t vsc;
   };
   // this thread's share of a tile: keys by 16 bytes, values by 4 tokens x 8 elements
   auto load_tile = [&](Staged &st, int tile, int pages) {
     const int64_t p0 = (int64_t)tile * TK;
+    // a token without a page reads page 0: no branch comes between the loads.  A
+    // page's rows take less than 2^31 bytes, so a row's place in it is 32 bits
     st.kok = st.vok = 0;
+    const uint32_t q0 = (uint32_t)p0;
+    const int left = tile < t_hi ? (int)min((int64_t)TK, total - p0) : 0;
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
-      const int tok = tid / (D / KE) + j * (kAttnBlock / (D / KE)), ch = tid % (D / KE);
-      const int64_t row = row_of(__shfl(pages, tok / 16, 64), p0 + tok);
-      if (row >= 0) {
-        st.kok |= 1 << j;
-        st.kreg[j] = *reinterpret_cast<const vec16 *>(cv.k + (row * D + ch * KE) * (kE4M3 ? 1 : 2));
-        if constexpr (kE4M3) st.ksc[j] = cv.k_scale[row];
-      }
+      const int tok = tid / (D / KE) + j * (kAttnLoaders / (D / KE)), ch = tid % (D / KE);
+      const int pg = __shfl(pages, tok / 16, 64);
+      const bool ok = tok < left && (uint32_t)pg < (uint32_t)cv.n_pages;
+      const uint32_t at = head_row + ((q0 + tok) & in_page), p_ = ok ? pg : 0;
+      st.kok |= ok << j;
+      st.kreg[j] = *reinterpret_cast<const vec16 *>(cv.k + (uint64_t)p_ * (page_rows * RB) +
+                                                    (at * RB + ch * 16));
+      if constexpr (kE4M3) st.ksc[j] = *(cv.k_scale + (uint64_t)p_ * page_rows + at);
     }
+    {
+      const int q = tid / (D / 8), ch = tid % (D / 8);
+      const int pg = __shfl(pages, q / 4, 64);  // 4 tokens, one page
+      const bool ok = 4 * q < left && (uint32_t)pg < (uint32_t)cv.n_pages;
+      const uint32_t at = head_row + ((q0 + 4 * q) & in_page), p_ = ok ? pg : 0;
+      st.vok = ok;
+      const uint8_t *v = cv.v + (uint64_t)p_ * (page_rows * RB) + (at * RB + ch * (RB / D * 8));
+      if constexpr (kE4M3) {
+        st.vsc = *reinterpret_cast<const uint32_t *>(cv.v_scale + (uint64_t)p_ * page_rows + at);
 #pragma unroll
-    for (int j = 0; j < VQ; ++j) {
-      const int q = tid / (D / 8) + j * (kAttnBlock / (D / 8)), ch = tid % (D / 8);
-      const int64_t row = row_of(__shfl(pages, q / 4, 64), p0 + 4 * q);  // 4 tokens, one page
-      if (row >= 0) {
-        st.vok |= 1 << j;
-        if constexpr (kE4M3) {
-          st.vsc[j] = *reinterpret_cast<const uint32_t *>(cv.v_scale + row);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const u32x2 x = *reinterpret_cast<const u32x2 *>(cv.v + (row + 2 * i) * D + ch * 8);
-            const u32x2 y = *reinterpret_cast<const u32x2 *>(cv.v + (row + 2 * i + 1) * D + ch * 8);
-            st.vreg[j][i] = u32x4{x.x, x.y, y.x, y.y};
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            st.vreg[j][i] = *reinterpret_cast<const vec16 *>(cv.v + ((row + i) * D + ch * 8) * 2);
+        for (int i = 0; i < 2; ++i) {
+          const u32x2 x = *reinterpret_cast<const u32x2 *>(v + 2 * i * RB);
+          const u32x2 y = *reinterpret_cast<const u32x2 *>(v + (2 * i + 1) * RB);
+          st.vreg[i] = u32x4{x.x, x.y, y.x, y.y};
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.vreg[i] = *reinterpret_cast<const vec16 *>(v + i * RB);
       }
     }
   };
   // registers to LDS.  A token without a valid page gets NaN keys, so that every row
   // that attends to it is NaN; values behind the end are zero.
-  auto store_tile = [&](const Staged &st, int tile, bool last) {
+  auto store_tile = [&](const Staged &st, int tile) {
+    const bool last = (int64_t)tile * TK + TK > ctx;  // holds nodes or the end
+    vec16 *const lk = reinterpret_cast<vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
+    unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
-      const int tok = tid / (D / KE) + j * (kAttnBlock / (D / KE)), ch = tid % (D / KE);
+      const int tok = tid / (D / KE) + j * (kAttnLoaders / (D / KE)), ch = tid % (D / KE);
       vec16 w[KE / 8];
       if (!((st.kok >> j) & 1)) {
 #pragma unroll
@@ -258,28 +272,27 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
         lk[tok * KB + ((ch * (KE / 8) + i) ^ (tok & (KB - 1)))] = w[i];
     }
     bool odd = false;
-#pragma unroll
-    for (int j = 0; j < VQ; ++j) {
-      const int q = tid / (D / 8) + j * (kAttnBlock / (D / 8)), ch = tid % (D / 8);
+    {
+      const int q = tid / (D / 8), ch = tid % (D / 8);
       uint32_t x[4][4];  // token, pair of neighbouring elements
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (kE4M3) {
-          const float sc = scale_factor((st.vsc[j] >> (8 * i)) & 255);
-          const uint32_t u = st.vreg[j][i / 2][2 * (i & 1)], v = st.vreg[j][i / 2][2 * (i & 1) + 1];
+          const float sc = scale_factor((st.vsc >> (8 * i)) & 255);
+          const uint32_t u = st.vreg[i / 2][2 * (i & 1)], v = st.vreg[i / 2][2 * (i & 1) + 1];
           x[i][0] = widen2<false>(u, sc);
           x[i][1] = widen2<true>(u, sc);
           x[i][2] = widen2<false>(v, sc);
           x[i][3] = widen2<true>(v, sc);
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] = st.vreg[j][i][e];
+          for (int e = 0; e < 4; ++e) x[i][e] = st.vreg[i][e];
         }
       }
       if (last) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool there = 4 * q + i < left && ((st.vok >> j) & 1);
+          const bool there = 4 * q + i < left && st.vok;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (!there) x[i][e] = 0;
@@ -312,6 +325,32 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
     if (odd) lds_odd = 1;
   };
 
+  Staged st[PF];
+  int pages = load_pages(t_lo);
+#pragma unroll
+  for (int k = 0; k < PF; ++k) {
+    const int next = load_pages(t_lo + k + 1);
+    load_tile(st[k], t_lo + k, pages);
+    pages = next;
+  }
+  for (int tile0 = t_lo; tile0 < t_hi; tile0 += PF)
+#pragma unroll
+    for (int k = 0; k < PF; ++k) {
+      const int tile = tile0 + k;
+      if (tile >= t_hi) break;
+      store_tile(st[k], tile);
+      // loads return in order: the pages of the tile after that go out first, or
+      // waiting for them would wait for this tile's data.  Behind the last tile the
+      // loads read page 0, so that no branch makes the waits wait for all
+      const int next = load_pages(tile + PF + 1);
+      load_tile(st[k], tile + PF, pages);
+      pages = next;
+      __syncthreads();  // this tile is there, and the one before it is done with
+    }
+  __syncthreads();  // the last tile is done with
+  }
+  } else {  // the waves that compute
+  const int wq = wave % WQ, wt = wave / WQ;
   vec16 qf[NT][ST];
   int node[NT];
 #pragma unroll
@@ -334,28 +373,13 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int W = (a.T + 31) / 32;
-
-  if (tid == 0) lds_odd = 0;
-  __syncthreads();
-  Staged st[PF];
-  int pages = load_pages(t_lo);
-#pragma unroll
-  for (int k = 0; k < PF; ++k) {
-    if (t_lo + k < t_hi) load_tile(st[k], t_lo + k, pages);
-    pages = load_pages(t_lo + k + 1);
-  }
-  for (int tile0 = t_lo; tile0 < t_hi; tile0 += PF)
-#pragma unroll
-  for (int k = 0; k < PF; ++k) {
-    const int tile = tile0 + k;
-    if (tile >= t_hi) break;
+  for (int tile = t_lo; tile < t_hi; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
     const bool last = p0 + TK > ctx;  // holds nodes or the end
-    store_tile(st[k], tile, last);
+    const vec16 *const lk =
+        reinterpret_cast<const vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
+    const unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     __syncthreads();
-    if (tile + PF < t_hi) load_tile(st[k], tile + PF, pages);
-    pages = load_pages(tile + PF + 1);
     if (active) {
 #pragma unroll
       for (int g0 = 0; g0 < TW; g0 += G) {
@@ -441,14 +465,27 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
         }
       }
     }
-    __syncthreads();
   }
+  if (t_lo < t_hi) __syncthreads();
+  float (*lo)[M][D + 4] = reinterpret_cast<float (*)[M][D + 4]>(lds);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] += __shfl_xor(l[t], 16, 64);
     l[t] += __shfl_xor(l[t], 32, 64);
-    if (bad) l[t] = nan;
+    const int R = (wq * NT + t) * 16 + n;
+    if (g == 0) {
+      lds_ms[wt][R][0] = base[t];
+      lds_ms[wt][R][1] = bad ? nan : l[t];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < DT; i += 4)
+        *reinterpret_cast<f32x4 *>(&lo[wt][R][DT * (4 * g + r) + i]) =
+            f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]};
   }
+  }
+  __syncthreads();
 
   // one row's 4 elements from d on, its exponent and its sum
   auto put = [&](int R, int d, f32x4 x, float mm, float ll, bool first) {
@@ -494,48 +531,32 @@ __global__ __launch_bounds__(kAttnBlock, 2) void kr_tree_attention(CacheView cv,
     }
     return x;
   };
-  // the waves that split the tokens join over the largest exponent, 16 * WQ rows at a time
-  float (*lo)[16 * WQ][D + 4] = reinterpret_cast<float (*)[16 * WQ][D + 4]>(lds);
+  // the waves that split the tokens join over the largest exponent
+  const float (*lo)[M][D + 4] = reinterpret_cast<const float (*)[M][D + 4]>(lds);
+  constexpr int V = D / 4;  // 16-byte pieces of a row
+  for (int i = threadIdx.x; i < M * V; i += Shape::kBlock) {
+    const int r = i / V, d = (i % V) * 4;
+    if (mt * M + r >= rows) break;
+    float mm = kNegInf, ll = 0.0f;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (t > 0) __syncthreads();
-    if (g == 0) {
-      lds_ms[wt][wq * 16 + n][0] = base[t];
-      lds_ms[wt][wq * 16 + n][1] = l[t];
+    for (int w = 0; w < WT; ++w) mm = fmaxf(mm, lds_ms[w][r][0]);
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < WT; ++w) {
+      const float f = part_factor(lds_ms[w][r][0], lds_ms[w][r][1], mm);
+      ll += lds_ms[w][r][1] * f;
+      x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int i = 0; i < DT; i += 4)
-        *reinterpret_cast<f32x4 *>(&lo[wt][wq * 16 + n][DT * (4 * g + r) + i]) =
-            f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]};
-    __syncthreads();
-    constexpr int V = D / 4;  // 16-byte pieces of a row
-    for (int i = tid; i < 16 * WQ * V; i += kAttnBlock) {
-      const int r = i / V, d = (i % V) * 4;
-      const int R = mt * M + ((r >> 4) * NT + t) * 16 + (r & 15);
-      if (R >= rows) continue;
-      float mm = kNegInf, ll = 0.0f;
-#pragma unroll
-      for (int w = 0; w < WT; ++w) mm = fmaxf(mm, lds_ms[w][r][0]);
-      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 0; w < WT; ++w) {
-        const float f = part_factor(lds_ms[w][r][0], lds_ms[w][r][1], mm);
-        ll += lds_ms[w][r][1] * f;
-        x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
-      }
-      if (lds_odd) x = odd_values(R, d, x, mm);
-      put(R, d, x, mm, ll, d == 0);
-    }
+    if (lds_odd) x = odd_values(mt * M + r, d, x, mm);
+    put(mt * M + r, d, x, mm, ll, d == 0);
   }
 }
 
 // The S parts of every row: D / 4 lanes per row.
 template <int D>
-__global__ __launch_bounds__(kAttnBlock) void kr_attn_join(AttnArgs a, int Hq) {
+__global__ __launch_bounds__(kAttnJoinBlock) void kr_attn_join(AttnArgs a, int Hq) {
   constexpr int L = D / 4;
-  const int64_t row = (int64_t)blockIdx.x * (kAttnBlock / L) + threadIdx.x / L;
+  const int64_t row = (int64_t)blockIdx.x * (kAttnJoinBlock / L) + threadIdx.x / L;
   if (row >= a.rows_all) return;
   const int d = (threadIdx.x % L) * 4;
   const int64_t bt = row / Hq;

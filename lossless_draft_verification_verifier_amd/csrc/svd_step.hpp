@@ -88,7 +88,7 @@ int read_kind(bool e4m3, int D, const CacheView &c, const int32_t *start, const 
 
 // Rows per workgroup and parts of an attention call: a function of the sizes alone.
 struct AttnPlan {
-  int nt, wq, m_tiles, S;
+  int nt, wq, wt, m_tiles, S;
 };
 
 constexpr int64_t kAttnTargetGroups = 1024;  // workgroups to aim for: four per CU
@@ -98,7 +98,8 @@ AttnPlan attn_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int64_t room) 
   AttnPlan p;
   const int64_t rows = (int64_t)T * (Hq / Hkv);
   p.nt = rows <= 64 ? 1 : 2;
-  p.wq = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  p.wq = rows <= 64 ? (int)((rows + 15) / 16) : 4;
+  p.wt = rows <= 32 ? 2 : 1;
   const int m = 16 * p.nt * p.wq;
   p.m_tiles = (int)((rows + m - 1) / m);
   const int64_t base = B * Hkv * p.m_tiles;
@@ -122,26 +123,27 @@ size_t attn_ms_offset(int64_t rows, int S, int D) {
   return align_up((size_t)rows * S * D * sizeof(float));
 }
 
-template <int D, bool kE4M3, int NT, int WQ>
+template <int D, bool kE4M3, int NT, int WQ, int WT>
 int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   CallTimer tm;
   const int64_t grid = ((int64_t)a.units + 7) / 8 * 8 * a.m_tiles;
-  SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ>,
-             dim3((unsigned)grid), dim3(kAttnBlock), s, c, a);
+  SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ, WT>,
+             dim3((unsigned)grid), dim3(AttnShape<D, kE4M3, NT, WQ, WT>::kBlock), s, c, a);
   if (a.S > 1) {
-    constexpr int rows = kAttnBlock / (D / 4);
+    constexpr int rows = kAttnJoinBlock / (D / 4);
     SVD_LAUNCH(tm, SVD_KERNEL_ATTENTION_JOIN, s, kr_attn_join<D>,
-               dim3((unsigned)((a.rows_all + rows - 1) / rows)), dim3(kAttnBlock), s, a, Hq);
+               dim3((unsigned)((a.rows_all + rows - 1) / rows)), dim3(kAttnJoinBlock), s, a, Hq);
   }
   return SVD_OK;
 }
 
 template <int D, bool kE4M3>
 int attn_rows(const AttnPlan &p, const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
-  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4>(c, a, Hq, s);
-  if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4>(c, a, Hq, s);
-  if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2>(c, a, Hq, s);
-  return attn_launch<D, kE4M3, 1, 1>(c, a, Hq, s);
+  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 1>(c, a, Hq, s);
+  if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4, 1>(c, a, Hq, s);
+  if (p.wq == 3) return attn_launch<D, kE4M3, 1, 3, 1>(c, a, Hq, s);
+  if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2, 2>(c, a, Hq, s);
+  return attn_launch<D, kE4M3, 1, 1, 2>(c, a, Hq, s);
 }
 
 template <typename E, bool kVec, bool kBias, int PATH>
