@@ -203,17 +203,27 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     uint32_t vsc;
   };
   // this thread's share of a tile: keys by 16 bytes, values by 4 tokens x 8 elements
-  auto load_tile = [&](Staged &st, int tile, int pages) {
+  // pages: the table's entries for it, replaced by those of tile + PF.  Loads return
+  // in order, so the entries go out before the tile's data: waiting for them must
+  // not wait for that
+  auto load_tile = [&](Staged &st, int tile, int &pages) {
     const int64_t p0 = (int64_t)tile * TK;
     // a token without a page reads page 0: no branch comes between the loads.  A
     // page's rows take less than 2^31 bytes, so a row's place in it is 32 bits
     st.kok = st.vok = 0;
     const uint32_t q0 = (uint32_t)p0;
     const int left = tile < t_hi ? (int)min((int64_t)TK, total - p0) : 0;
+    int pk[KL];
+#pragma unroll
+    for (int j = 0; j < KL; ++j)
+      pk[j] = __shfl(pages, (tid / (D / KE) + j * (kAttnLoaders / (D / KE))) / 16, 64);
+    const int pv = __shfl(pages, tid / (D / 8) / 4, 64);  // 4 tokens, one page
+    pages = load_pages(tile + PF);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       const int tok = tid / (D / KE) + j * (kAttnLoaders / (D / KE)), ch = tid % (D / KE);
-      const int pg = __shfl(pages, tok / 16, 64);
+      const int pg = pk[j];
       const bool ok = tok < left && (uint32_t)pg < (uint32_t)cv.n_pages;
       const uint32_t at = head_row + ((q0 + tok) & in_page), p_ = ok ? pg : 0;
       st.kok |= ok << j;
@@ -223,7 +233,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     }
     {
       const int q = tid / (D / 8), ch = tid % (D / 8);
-      const int pg = __shfl(pages, q / 4, 64);  // 4 tokens, one page
+      const int pg = pv;
       const bool ok = 4 * q < left && (uint32_t)pg < (uint32_t)cv.n_pages;
       const uint32_t at = head_row + ((q0 + 4 * q) & in_page), p_ = ok ? pg : 0;
       st.vok = ok;
@@ -241,6 +251,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
         for (int i = 0; i < 4; ++i) st.vreg[i] = *reinterpret_cast<const vec16 *>(v + i * RB);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   // registers to LDS.  A token without a valid page gets NaN keys, so that every row
   // that attends to it is NaN; values behind the end are zero.
@@ -249,14 +260,12 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     vec16 *const lk = reinterpret_cast<vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
+    const bool gaps = __any(st.kok != (1 << KL) - 1);
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       const int tok = tid / (D / KE) + j * (kAttnLoaders / (D / KE)), ch = tid % (D / KE);
       vec16 w[KE / 8];
-      if (!((st.kok >> j) & 1)) {
-#pragma unroll
-        for (int i = 0; i < KE / 8; ++i) w[i] = vec16{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
-      } else if constexpr (kE4M3) {
+      if constexpr (kE4M3) {
         const float sc = scale_factor(st.ksc[j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -266,6 +275,11 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
         }
       } else {
         w[0] = st.kreg[j];
+      }
+      if (gaps && !((st.kok >> j) & 1)) {
+#pragma unroll
+        for (int i = 0; i < KE / 8; ++i)
+          w[i] = vec16{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
       }
 #pragma unroll
       for (int i = 0; i < KE / 8; ++i)
@@ -326,25 +340,20 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   };
 
   Staged st[PF];
-  int pages = load_pages(t_lo);
+  int pages[PF];
 #pragma unroll
-  for (int k = 0; k < PF; ++k) {
-    const int next = load_pages(t_lo + k + 1);
-    load_tile(st[k], t_lo + k, pages);
-    pages = next;
-  }
+  for (int k = 0; k < PF; ++k) pages[k] = load_pages(t_lo + k);
+#pragma unroll
+  for (int k = 0; k < PF; ++k) load_tile(st[k], t_lo + k, pages[k]);
   for (int tile0 = t_lo; tile0 < t_hi; tile0 += PF)
 #pragma unroll
     for (int k = 0; k < PF; ++k) {
       const int tile = tile0 + k;
-      if (tile >= t_hi) break;
-      store_tile(st[k], tile);
-      // loads return in order: the pages of the tile after that go out first, or
-      // waiting for them would wait for this tile's data.  Behind the last tile the
-      // loads read page 0, so that no branch makes the waits wait for all
-      const int next = load_pages(tile + PF + 1);
-      load_tile(st[k], tile + PF, pages);
-      pages = next;
+      // the steps are a multiple of PF, and behind the last tile the loads read page 0:
+      // with a way out between them, or one around the loads, the waits of the next
+      // tile would have to wait for all that is on its way
+      if (tile < t_hi) store_tile(st[k], tile);
+      load_tile(st[k], tile + PF, pages[k]);
       __syncthreads();  // this tile is there, and the one before it is done with
     }
   __syncthreads();  // the last tile is done with
@@ -373,14 +382,15 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  for (int tile = t_lo; tile < t_hi; ++tile) {
+  const int steps = (t_hi - t_lo + PF - 1) / PF * PF;  // as the loading waves take
+  for (int tile = t_lo; tile < t_lo + steps; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
     const bool last = p0 + TK > ctx;  // holds nodes or the end
     const vec16 *const lk =
         reinterpret_cast<const vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     const unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     __syncthreads();
-    if (active) {
+    if (active && tile < t_hi) {
 #pragma unroll
       for (int g0 = 0; g0 < TW; g0 += G) {
         const int k0 = wt * TW + g0;  // first token of the step within the tile
