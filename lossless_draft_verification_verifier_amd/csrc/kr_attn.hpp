@@ -47,7 +47,7 @@ struct AttnArgs {
   const int32_t *ctx_len, *n_nodes, *table;
   const uint32_t *anc;      // [B][T][W] or null: a chain
   int64_t room;             // positions of a sequence's pages
-  int T, group, S, m_tiles, units;  // units = B * Hkv * S
+  int T, group, S, m_tiles, m_rows, units;  // units = B * Hkv * S
   float c;                  // scale * log2(e)
   uint16_t *out;            // [B][T][Hq][D]
   float *lse;               // [B][T][Hq] or null
@@ -69,6 +69,16 @@ __device__ __forceinline__ float scale_factor(uint32_t byte) {  // of a byte fro
 template <bool kHigh>
 __device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, kHigh));
+}
+
+// The maximum over the 4 lanes that hold a row (lane % 16): two exchanges of half
+// the lanes, which stay in the vector unit.
+__device__ __forceinline__ float row_max(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t v = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 // What a part (exponent m, sum l) is scaled by under the common exponent mm.  A
@@ -125,10 +135,11 @@ __device__ __forceinline__ uint32_t allow_window(const uint32_t *words, int W, i
 template <int D, bool kE4M3, int NT, int WQ, int WT>
 struct AttnShape {
   static constexpr int TK = 8192 / D;                 // tokens per tile: 32 KB of K and V
-  static constexpr int M = 16 * NT * WQ;              // rows per workgroup
+  static constexpr int M = 16 * NT * WQ;              // most rows per workgroup
   static constexpr int NC = WQ * WT;                  // computing waves
-  static constexpr int kBlock = kAttnLoaders + 64 * NC;
-  static constexpr int PF = kE4M3 ? 3 : 2;            // tiles on their way at a time
+  static constexpr bool kRoles = NT == 1;             // loading waves of their own
+  static constexpr int kBlock = 64 * NC + (kRoles ? kAttnLoaders : 0);
+  static constexpr int PF = !kRoles ? 1 : kE4M3 ? 3 : 2;  // tiles on their way at a time
   static constexpr int kMinWaves = NT == 1 ? 4 : 2;   // per SIMD
   static constexpr int kTileBytes = 2 * TK * D * 2;
   static constexpr int kJoinBytes = WT * M * (D + 4) * 4;
@@ -141,15 +152,17 @@ __global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
 void kr_tree_attention(CacheView cv, AttnArgs a) {
   using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
   constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
+  constexpr bool kRoles = Shape::kRoles;
   constexpr int DT = D / 16, ST = D / 32;
   constexpr int KB = D / 8;               // 16-byte blocks of a key row in LDS
   constexpr int VB = TK / 8;              // 16-byte blocks of a row of V^T in LDS
   constexpr int TW = TK / WT;             // tokens of a wave
-  constexpr int G = TW >= 64 && NT <= 2 ? 64 : 32;    // tokens per softmax step
+  constexpr int G = TW >= 64 ? 64 : 32;   // tokens per softmax step
   constexpr int KE = kE4M3 ? 16 : 8;      // key elements per 16-byte load
   constexpr int KL = TK * D / KE / kAttnLoaders;      // key loads per thread
   // values: one piece of 4 tokens x 8 elements per thread
   static_assert(KL >= 1 && TK * D == 32 * kAttnLoaders && TW % 32 == 0, "");
+  static_assert(kRoles || Shape::kBlock == 2 * kAttnLoaders, "half of the waves bring keys, half values");
   __shared__ __align__(16) unsigned char lds[Shape::kLdsBytes];
   __shared__ float lds_ms[WT][M][2];
   __shared__ int lds_odd;                 // some node of this part has a value that is not finite
@@ -168,7 +181,8 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // lengths out of range: every row of the prefix is NaN
   const bool bad = attn_bad(ctx, nodes, a.T, a.room);
   const int rows = (bad ? a.T : nodes) * a.group;
-  if (mt * M >= rows) return;
+  const int r_lo = mt * a.m_rows, r_hi = min(r_lo + a.m_rows, rows);  // this workgroup's rows
+  if (r_lo >= r_hi) return;
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int W = (a.T + 31) / 32;
@@ -181,9 +195,10 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   if (threadIdx.x == 0) lds_odd = 0;
   __syncthreads();
 
-  if (wave >= Shape::NC) {  // the waves that bring tiles to LDS
-  if (t_lo < t_hi) {
-  const int tid = threadIdx.x - 64 * Shape::NC;
+  // the threads that bring a tile to LDS: the loading waves do keys and values,
+  // without them waves 0 to 3 do values and waves 4 to 7 keys
+  const int tid = kRoles ? (int)threadIdx.x - 64 * Shape::NC : (int)threadIdx.x & (kAttnLoaders - 1);
+  const bool do_k = kRoles || wave >= kAttnLoaders / 64, do_v = kRoles || !do_k;
   // the table's entry for 16-token block `lane` of a tile.  It is looked at when the
   // tile is loaded, not here: that would wait for it
   const int32_t *table = a.table + b * cv.max_pages;
@@ -196,11 +211,11 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   constexpr uint32_t RB = kE4M3 ? D : 2 * D;  // bytes of a row
   const uint32_t page_rows = (uint32_t)cv.Hkv << cv.page_shift, head_row = (uint32_t)h << cv.page_shift;
 
+  constexpr int VO = kRoles ? KL : 0;  // where values are held: with the keys, or in their place
   struct Staged {  // a thread's share of a tile on its way to LDS
-    vec16 kreg[KL];
-    u32x4 vreg[kE4M3 ? 2 : 4];
-    int ksc[KL], kok, vok;
-    uint32_t vsc;
+    vec16 reg[VO + KL];
+    uint32_t scale[VO ? KL + 1 : KL];
+    int kok, vok;
   };
   // this thread's share of a tile: keys by 16 bytes, values by 4 tokens x 8 elements
   // pages: the table's entries for it, replaced by those of tile + PF.  Loads return
@@ -220,6 +235,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     const int pv = __shfl(pages, tid / (D / 8) / 4, 64);  // 4 tokens, one page
     pages = load_pages(tile + PF);
     __builtin_amdgcn_sched_barrier(0);
+    if (do_k) {
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       const int tok = tid / (D / KE) + j * (kAttnLoaders / (D / KE)), ch = tid % (D / KE);
@@ -227,11 +243,12 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       const bool ok = tok < left && (uint32_t)pg < (uint32_t)cv.n_pages;
       const uint32_t at = head_row + ((q0 + tok) & in_page), p_ = ok ? pg : 0;
       st.kok |= ok << j;
-      st.kreg[j] = *reinterpret_cast<const vec16 *>(cv.k + (uint64_t)p_ * (page_rows * RB) +
+      st.reg[j] = *reinterpret_cast<const vec16 *>(cv.k + (uint64_t)p_ * (page_rows * RB) +
                                                     (at * RB + ch * 16));
-      if constexpr (kE4M3) st.ksc[j] = *(cv.k_scale + (uint64_t)p_ * page_rows + at);
+      if constexpr (kE4M3) st.scale[j] = *(cv.k_scale + (uint64_t)p_ * page_rows + at);
     }
-    {
+    }
+    if (do_v) {
       const int q = tid / (D / 8), ch = tid % (D / 8);
       const int pg = pv;
       const bool ok = 4 * q < left && (uint32_t)pg < (uint32_t)cv.n_pages;
@@ -239,16 +256,16 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       st.vok = ok;
       const uint8_t *v = cv.v + (uint64_t)p_ * (page_rows * RB) + (at * RB + ch * (RB / D * 8));
       if constexpr (kE4M3) {
-        st.vsc = *reinterpret_cast<const uint32_t *>(cv.v_scale + (uint64_t)p_ * page_rows + at);
+        st.scale[VO] = *reinterpret_cast<const uint32_t *>(cv.v_scale + (uint64_t)p_ * page_rows + at);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const u32x2 x = *reinterpret_cast<const u32x2 *>(v + 2 * i * RB);
           const u32x2 y = *reinterpret_cast<const u32x2 *>(v + (2 * i + 1) * RB);
-          st.vreg[i] = u32x4{x.x, x.y, y.x, y.y};
+          st.reg[VO + i] = vec16{x.x, x.y, y.x, y.y};
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st.vreg[i] = *reinterpret_cast<const vec16 *>(v + i * RB);
+        for (int i = 0; i < 4; ++i) st.reg[VO + i] = *reinterpret_cast<const vec16 *>(v + i * RB);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -261,20 +278,21 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
     const bool gaps = __any(st.kok != (1 << KL) - 1);
+    if (do_k) {
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       const int tok = tid / (D / KE) + j * (kAttnLoaders / (D / KE)), ch = tid % (D / KE);
       vec16 w[KE / 8];
       if constexpr (kE4M3) {
-        const float sc = scale_factor(st.ksc[j]);
+        const float sc = scale_factor(st.scale[j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t x = i ? st.kreg[j].z : st.kreg[j].x, y = i ? st.kreg[j].w : st.kreg[j].y;
+          const uint32_t x = i ? st.reg[j].z : st.reg[j].x, y = i ? st.reg[j].w : st.reg[j].y;
           w[i] = vec16{widen2<false>(x, sc), widen2<true>(x, sc), widen2<false>(y, sc),
                        widen2<true>(y, sc)};
         }
       } else {
-        w[0] = st.kreg[j];
+        w[0] = st.reg[j];
       }
       if (gaps && !((st.kok >> j) & 1)) {
 #pragma unroll
@@ -285,22 +303,23 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       for (int i = 0; i < KE / 8; ++i)
         lk[tok * KB + ((ch * (KE / 8) + i) ^ (tok & (KB - 1)))] = w[i];
     }
+    }
     bool odd = false;
-    {
+    if (do_v) {
       const int q = tid / (D / 8), ch = tid % (D / 8);
       uint32_t x[4][4];  // token, pair of neighbouring elements
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (kE4M3) {
-          const float sc = scale_factor((st.vsc >> (8 * i)) & 255);
-          const uint32_t u = st.vreg[i / 2][2 * (i & 1)], v = st.vreg[i / 2][2 * (i & 1) + 1];
+          const float sc = scale_factor((st.scale[VO] >> (8 * i)) & 255);
+          const uint32_t u = st.reg[VO + i / 2][2 * (i & 1)], v = st.reg[VO + i / 2][2 * (i & 1) + 1];
           x[i][0] = widen2<false>(u, sc);
           x[i][1] = widen2<true>(u, sc);
           x[i][2] = widen2<false>(v, sc);
           x[i][3] = widen2<true>(v, sc);
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] = st.vreg[i][e];
+          for (int e = 0; e < 4; ++e) x[i][e] = st.reg[VO + i][e];
         }
       }
       if (last) {
@@ -339,32 +358,14 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     if (odd) lds_odd = 1;
   };
 
-  Staged st[PF];
-  int pages[PF];
-#pragma unroll
-  for (int k = 0; k < PF; ++k) pages[k] = load_pages(t_lo + k);
-#pragma unroll
-  for (int k = 0; k < PF; ++k) load_tile(st[k], t_lo + k, pages[k]);
-  for (int tile0 = t_lo; tile0 < t_hi; tile0 += PF)
-#pragma unroll
-    for (int k = 0; k < PF; ++k) {
-      const int tile = tile0 + k;
-      // the steps are a multiple of PF, and behind the last tile the loads read page 0:
-      // with a way out between them, or one around the loads, the waits of the next
-      // tile would have to wait for all that is on its way
-      if (tile < t_hi) store_tile(st[k], tile);
-      load_tile(st[k], tile + PF, pages[k]);
-      __syncthreads();  // this tile is there, and the one before it is done with
-    }
-  __syncthreads();  // the last tile is done with
-  }
-  } else {  // the waves that compute
+  // the waves that compute: their rows, a loop over the tiles, the parts to LDS
+  auto compute = [&](auto &&begin, auto &&end) {
   const int wq = wave % WQ, wt = wave / WQ;
   vec16 qf[NT][ST];
   int node[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = min(mt * M + (wq * NT + t) * 16 + n, rows - 1);
+    const int r = min(r_lo + (wq * NT + t) * 16 + n, r_hi - 1);
     node[t] = r / a.group;
     const uint16_t *q = a.q + (b * a.T + node[t]) * a.q_stride +
                         (int64_t)(h * a.group + r % a.group) * D;
@@ -372,7 +373,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     for (int i = 0; i < ST; ++i) qf[t][i] = *reinterpret_cast<const vec16 *>(q + 32 * i + 8 * g);
   }
   // rows of this wave that exist
-  const bool active = mt * M + wq * NT * 16 < rows;
+  const bool active = r_lo + wq * NT * 16 < r_hi;
   f32x4 o[NT][DT];
   float base[NT], l[NT];  // base: the exponent that l and o are held over
 #pragma unroll
@@ -383,13 +384,14 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   const int steps = (t_hi - t_lo + PF - 1) / PF * PF;  // as the loading waves take
+  if (t_lo < t_hi) begin();
   for (int tile = t_lo; tile < t_lo + steps; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
     const bool last = p0 + TK > ctx;  // holds nodes or the end
     const vec16 *const lk =
         reinterpret_cast<const vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     const unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
-    __syncthreads();
+    if constexpr (kRoles) __syncthreads();
     if (active && tile < t_hi) {
 #pragma unroll
       for (int g0 = 0; g0 < TW; g0 += G) {
@@ -425,7 +427,10 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
                   if (!((ok >> (16 * u + 4 * g + r)) & 1u)) sc[t][2 * w + u][r] = kNegInf;
             }
         }
-        vec16 pf[NT][G / 32];
+        // the exponent moves when a score passes it by 2^8: p, l and o lose nothing to
+        // a factor of at most 256, and most steps rescale nothing
+        float next[NT];
+        bool moves = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float mx = kNegInf;
@@ -433,19 +438,23 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
           for (int u = 0; u < G / 16; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[t][u][r]);
-          mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-          mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-          // the exponent moves when a score passes it by 2^8: p, l and o lose nothing to
-          // a factor of at most 256, and most steps rescale nothing
-          const float next = mx * a.c;
-          const bool move = next > base[t] + 8.0f;
-          if (__any(move)) {
-            const float f = move ? fast_exp2(base[t] - next) : 1.0f;
+          next[t] = row_max(mx) * a.c;
+          moves |= next[t] > base[t] + 8.0f;
+        }
+        if (__any(moves)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const bool move = next[t] > base[t] + 8.0f;
+            const float f = move ? fast_exp2(base[t] - next[t]) : 1.0f;
             l[t] *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[t][i] *= f;
-            base[t] = move ? next : base[t];
+            base[t] = move ? next[t] : base[t];
           }
+        }
+        vec16 pf[NT][G / 32];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
           const float sub = base[t] == kNegInf ? 0.0f : base[t];
 #pragma unroll
           for (int u = 0; u < G / 16; ++u)
@@ -475,8 +484,9 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
         }
       }
     }
+    end(tile);
   }
-  if (t_lo < t_hi) __syncthreads();
+  if (kRoles && t_lo < t_hi) __syncthreads();
   float (*lo)[M][D + 4] = reinterpret_cast<float (*)[M][D + 4]>(lds);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -494,6 +504,43 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
         *reinterpret_cast<f32x4 *>(&lo[wt][R][DT * (4 * g + r) + i]) =
             f32x4{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]};
   }
+  };
+  Staged st[PF];
+  int pages[PF];
+  if constexpr (kRoles) {
+    if (wave < Shape::NC) {
+      compute([] {}, [](int) {});
+    } else if (t_lo < t_hi) {
+#pragma unroll
+      for (int k = 0; k < PF; ++k) pages[k] = load_pages(t_lo + k);
+#pragma unroll
+      for (int k = 0; k < PF; ++k) load_tile(st[k], t_lo + k, pages[k]);
+      for (int tile0 = t_lo; tile0 < t_hi; tile0 += PF)
+#pragma unroll
+        for (int k = 0; k < PF; ++k) {
+          const int tile = tile0 + k;
+          // the steps are a multiple of PF, and behind the last tile the loads read page 0:
+          // with a way out between them, or one around the loads, the waits of the next
+          // tile would have to wait for all that is on its way
+          if (tile < t_hi) store_tile(st[k], tile);
+          load_tile(st[k], tile + PF, pages[k]);
+          __syncthreads();  // this tile is there, and the one before it is done with
+        }
+      __syncthreads();  // the last tile is done with
+    }
+  } else {
+    auto bring = [&](int tile) {  // tile to LDS, the one after it on its way
+      if (tile < t_hi) store_tile(st[0], tile);
+      load_tile(st[0], tile + 1, pages[0]);
+      __syncthreads();
+    };
+    compute(
+        [&] {
+          pages[0] = load_pages(t_lo);
+          load_tile(st[0], t_lo, pages[0]);
+          bring(t_lo);
+        },
+        [&](int tile) { bring(tile + 1); });
   }
   __syncthreads();
 
@@ -546,7 +593,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   constexpr int V = D / 4;  // 16-byte pieces of a row
   for (int i = threadIdx.x; i < M * V; i += Shape::kBlock) {
     const int r = i / V, d = (i % V) * 4;
-    if (mt * M + r >= rows) break;
+    if (r_lo + r >= r_hi) break;
     float mm = kNegInf, ll = 0.0f;
 #pragma unroll
     for (int w = 0; w < WT; ++w) mm = fmaxf(mm, lds_ms[w][r][0]);
@@ -557,8 +604,8 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       ll += lds_ms[w][r][1] * f;
       x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
     }
-    if (lds_odd) x = odd_values(mt * M + r, d, x, mm);
-    put(mt * M + r, d, x, mm, ll, d == 0);
+    if (lds_odd) x = odd_values(r_lo + r, d, x, mm);
+    put(r_lo + r, d, x, mm, ll, d == 0);
   }
 }
 

@@ -88,7 +88,7 @@ int read_kind(bool e4m3, int D, const CacheView &c, const int32_t *start, const 
 
 // Rows per workgroup and parts of an attention call: a function of the sizes alone.
 struct AttnPlan {
-  int nt, wq, wt, m_tiles, S;
+  int nt, wq, wt, m_tiles, m_rows, S;
 };
 
 constexpr int64_t kAttnTargetGroups = 1024;  // workgroups to aim for: four per CU
@@ -98,10 +98,13 @@ AttnPlan attn_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int64_t room) 
   AttnPlan p;
   const int64_t rows = (int64_t)T * (Hq / Hkv);
   p.nt = rows <= 64 ? 1 : 2;
-  p.wq = rows <= 64 ? (int)((rows + 15) / 16) : 4;
-  p.wt = rows <= 32 ? 2 : 1;
+  p.wq = rows <= 64 ? (int)((rows + 15) / 16) : rows <= 128 ? 4 : 8;
+  p.wt = rows <= 32 || (p.nt == 2 && p.wq == 4) ? 2 : 1;
   const int m = 16 * p.nt * p.wq;
   p.m_tiles = (int)((rows + m - 1) / m);
+  const int unit = 16 * p.nt;  // rows of a wave: the workgroups share them evenly
+  const int64_t waves = (rows + unit - 1) / unit;
+  p.m_rows = (int)((waves + p.m_tiles - 1) / p.m_tiles) * unit;
   const int64_t base = B * Hkv * p.m_tiles;
   const int64_t most = std::max<int64_t>(1, room / kAttnPartTokens);
   const int64_t want = (kAttnTargetGroups + base - 1) / base;
@@ -139,7 +142,8 @@ int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
 
 template <int D, bool kE4M3>
 int attn_rows(const AttnPlan &p, const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
-  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 1>(c, a, Hq, s);
+  if (p.nt == 2 && p.wq == 8) return attn_launch<D, kE4M3, 2, 8, 1>(c, a, Hq, s);
+  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 2>(c, a, Hq, s);
   if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4, 1>(c, a, Hq, s);
   if (p.wq == 3) return attn_launch<D, kE4M3, 1, 3, 1>(c, a, Hq, s);
   if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2, 2>(c, a, Hq, s);
@@ -273,6 +277,7 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
   a.group = q_heads / c.Hkv;
   a.S = p.S;
   a.m_tiles = p.m_tiles;
+  a.m_rows = p.m_rows;
   a.units = (int)(B * c.Hkv * p.S);
   a.c = cs;
   a.out = static_cast<uint16_t *>(out);
