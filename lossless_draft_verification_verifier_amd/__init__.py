@@ -333,6 +333,7 @@ class Library:
 
 
 _default = Library(LIB_PATH)
+_c = _default._lib
 _timed = []
 
 
@@ -695,38 +696,58 @@ def adl_next(drafts, selected, accept_len, avg, gamma_b=None, eos=-1, k_min=1, k
 
 # --------------------------------------------------------------------------
 # Around the verification step: the draft tree, the paged cache, the attention
-# of the tree over it, and the adjustments of the verifier's logits
+# of the tree over it, and the adjustments of the verifier's logits.
+#
+# A decode step makes these calls on small tensors, where the host's share is
+# what counts: one check per tensor, pointers passed as they are, the current
+# stream's handle taken without a Stream object.
 
-def _ints(dev, **tensors):
-    """Check int32 tensors (None is allowed) and where they are."""
-    import torch
-    for n, t in tensors.items():
-        if t is None:
-            continue
-        _check(t, n, dev)
-        if t.dtype != torch.int32:
-            raise TypeError("%s must be int32" % n)
+_T = None  # torch, once a convenience has been called
 
 
-def _shaped(shape, **tensors):
-    for n, t in tensors.items():
-        if t is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError("%s must be %s, got %s" % (n, list(shape), list(t.shape)))
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
 
 
-def _on(dev, stream):
-    """The stream's handle (default: the device's current one)."""
-    import torch
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+def _bad(t, name, dev, dtype, shape):
+    """Say what is wrong with a tensor that failed its check."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev if dev.type == "cuda" else "the GPU"))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _call_on(dev, f, *args):
-    """f(*args) with dev as the current device."""
-    import torch
-    if dev.index == torch.cuda.current_device():
-        return f(*args)
-    with torch.cuda.device(dev):
-        return f(*args)
+def _ptr(t, name, dev, dtype, shape):
+    """Address of a contiguous tensor of this device, dtype and shape, or None."""
+    if t is None:
+        return None
+    if (t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous() or
+            dev.type != "cuda"):
+        _bad(t, name, dev, dtype, shape)
+    return t.data_ptr()
+
+
+def _call(f, name, dev, stream, *args):
+    """f(*args, stream) with dev as the current device; stream: default the current one."""
+    C = _torch()._C
+    if stream is None:
+        stream = C._cuda_getCurrentRawStream(dev.index)
+    elif not isinstance(stream, int):
+        stream = _addr(stream)
+    if C._cuda_getDevice() == dev.index:
+        rc = f(*args, stream)
+    else:
+        with _T.cuda.device(dev):
+            rc = f(*args, stream)
+    if rc != SVD_OK:
+        raise SvdError(rc, name)
 
 
 def draft_tree(drafts, root=None, n_max=None, stream=None):
@@ -735,37 +756,35 @@ def draft_tree(drafts, root=None, n_max=None, stream=None):
     suffices).  Returns tokens, parent, depth [B,n_max], anc [B,n_max,W] (bit i % 32
     of word i // 32: node i is on the node's path), n_nodes [B] and p_index
     [B,K,gamma+1], the rows of the pool [B * n_max, V] for select_and_verify_rows."""
-    import torch
-    dev = drafts.device
-    _ints(dev, drafts=drafts, root=root)
+    torch = _torch()
+    dev, i32 = drafts.device, torch.int32
     if drafts.dim() != 3:
         raise ValueError("drafts must be [B,K,gamma]")
     B, K, G = drafts.shape
-    _shaped((B,), root=root)
+    d = _ptr(drafts, "drafts", dev, i32, drafts.shape)
+    r = _ptr(root, "root", dev, i32, (B,))
     T = 1 + K * G if n_max is None else int(n_max)
     W = (T + 31) // 32
-    flat = torch.empty(B * (3 * T + T * W + 1 + K * (G + 1)) if T > 0 else 0, dtype=torch.int32,
-                       device=dev)
-    out, at = {}, 0
-    for name, shape in (("tokens", (B, T)), ("parent", (B, T)), ("depth", (B, T)),
-                        ("anc", (B, T, W)), ("n_nodes", (B,)), ("p_index", (B, K, G + 1))):
-        n = 1
-        for d in shape:
-            n *= d
-        out[name] = flat[at:at + n].view(shape) if T > 0 else flat
-        at += n
-    rc = _call_on(dev, svd_draft_tree, drafts, root, B, K, G, T, out["tokens"], out["parent"],
-                  out["depth"], out["anc"], out["n_nodes"], out["p_index"], _on(dev, stream))
-    if rc != SVD_OK:
-        raise SvdError(rc, "svd_draft_tree")
-    return out
+    BT, P = B * T, K * (G + 1)
+    # one allocation: tokens, parent, depth, anc, p_index, n_nodes
+    o1, o2, o3 = BT, 2 * BT, 3 * BT
+    o4 = o3 + BT * W
+    o5 = o4 + B * P
+    flat = torch.empty(max(o5 + B, 0), dtype=i32, device=dev)
+    at = flat.data_ptr()
+    _call(_c.svd_draft_tree, "svd_draft_tree", dev, stream, d, r, B, K, G, T, at, at + 4 * o1,
+          at + 4 * o2, at + 4 * o3, at + 4 * o5, at + 4 * o4)
+    view = flat.as_strided
+    return {"tokens": view((B, T), (T, 1)), "parent": view((B, T), (T, 1), o1),
+            "depth": view((B, T), (T, 1), o2), "anc": view((B, T, W), (T * W, W, 1), o3),
+            "n_nodes": view((B,), (1,), o5), "p_index": view((B, K, G + 1), (P, G + 1, 1), o4)}
 
 
 def kv_cache(n_pages, kv_heads, page, head_dim, dtype=None, device="cuda"):
     """An empty paged cache: k and v [n_pages,kv_heads,page,head_dim] of
     torch.bfloat16 (the default) or torch.float8_e4m3fn, and for the latter
     k_scale and v_scale [n_pages,kv_heads,page] uint8 (exponent + 127)."""
-    import torch
+    torch = _torch()
     dtype = torch.bfloat16 if dtype is None else dtype
     if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
         raise TypeError("a cache is torch.bfloat16 or torch.float8_e4m3fn, got %s" % dtype)
@@ -778,40 +797,39 @@ def kv_cache(n_pages, kv_heads, page, head_dim, dtype=None, device="cuda"):
 
 
 def _cache_struct(cache, block_table, B):
-    import torch
-    k, v, ks, vs = cache["k"], cache["v"], cache.get("k_scale"), cache.get("v_scale")
-    dev = k.device
-    for t, n in ((k, "cache k"), (v, "cache v")):
-        _check(t, n, dev)
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("cache k and v must be [n_pages,kv_heads,page,head_dim] of one dtype")
-    if k.dtype == torch.bfloat16:
+    """(the C struct of a cache and its block table, its device)."""
+    torch = _torch()
+    k, v = cache["k"], cache["v"]
+    dev, dtype, shape = k.device, k.dtype, k.shape
+    if len(shape) != 4:
+        raise ValueError("cache k and v must be [n_pages,kv_heads,page,head_dim]")
+    if dtype == torch.float8_e4m3fn:
+        code, ks, vs = SVD_CACHE_E4M3, cache["k_scale"], cache["v_scale"]
+        ks = _ptr(ks, "cache k_scale", dev, torch.uint8, shape[:3])
+        vs = _ptr(vs, "cache v_scale", dev, torch.uint8, shape[:3])
+    elif dtype == torch.bfloat16:
         code, ks, vs = SVD_CACHE_BF16, None, None
-    elif k.dtype == torch.float8_e4m3fn:
-        code = SVD_CACHE_E4M3
-        for t, n in ((ks, "cache k_scale"), (vs, "cache v_scale")):
-            if t is None or t.dtype != torch.uint8:
-                raise TypeError("%s must be uint8" % n)
-            _check(t, n, dev)
-            if t.shape != k.shape[:3]:
-                raise ValueError("%s must be [n_pages,kv_heads,page]" % n)
     else:
-        raise TypeError("a cache is torch.bfloat16 or torch.float8_e4m3fn, got %s" % k.dtype)
-    _ints(dev, block_table=block_table)
+        raise TypeError("a cache is torch.bfloat16 or torch.float8_e4m3fn, got %s" % dtype)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B,max_pages]")
-    n_pages, heads, page, D = k.shape
-    return CacheStruct(_addr(k), _addr(v), _addr(ks), _addr(vs), _addr(block_table), n_pages,
-                       block_table.shape[1], page, heads, D, code)
+    n_pages, heads, page, D = shape
+    mp = block_table.shape[1]
+    return CacheStruct(_ptr(k, "cache k", dev, dtype, shape), _ptr(v, "cache v", dev, dtype, shape),
+                       ks, vs, _ptr(block_table, "block_table", dev, torch.int32, (B, mp)),
+                       n_pages, mp, page, heads, D, code), dev
 
 
-def _token_stride(t, name, heads, D, dev):
+def _tokens(t, name, heads, D, dev):
     """Elements between the tokens of t [B,T,heads,D], whose heads are contiguous."""
-    if not t.is_cuda or t.device != dev:
-        raise ValueError("%s must be on %s" % (name, dev))
-    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != D:
-        raise ValueError("%s must be [B,T,%d,%d], got %s" % (name, heads, D, list(t.shape)))
-    B, T = t.shape[:2]
+    if t.device != dev or not t.is_cuda:
+        raise ValueError("%s must be on %s" % (name, dev if dev.type == "cuda" else "the GPU"))
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != D:
+        raise ValueError("%s must be [B,T,%d,%d], got %s" % (name, heads, D, list(shape)))
+    if t.is_contiguous():
+        return heads * D
+    B, T = shape[:2]
     sb, st, sh, sd = t.stride()
     if (D > 1 and sd != 1) or (heads > 1 and sh != D):
         raise ValueError("the heads of a token of %s must be contiguous" % name)
@@ -827,52 +845,45 @@ def cache_write(cache, k, v, block_table, ctx_len, n_new=None, dst=None, stream=
     a fused projection) to positions ctx_len[b] + t, or ctx_len[b] + dst[b,t] where
     dst is not negative; n_new [B] limits the tokens of a sequence.  cache: as from
     kv_cache; block_table [B,max_pages], ctx_len [B], dst [B,T] int32."""
-    dev = cache["k"].device
+    i32 = _torch().int32
     B, T = k.shape[:2]
-    c = _cache_struct(cache, block_table, B)
-    ks = _token_stride(k, "k", c.kv_heads, c.head_dim, dev)
-    vs = _token_stride(v, "v", c.kv_heads, c.head_dim, dev)
+    c, dev = _cache_struct(cache, block_table, B)
+    ks = _tokens(k, "k", c.kv_heads, c.head_dim, dev)
+    vs = _tokens(v, "v", c.kv_heads, c.head_dim, dev)
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must share one shape and dtype")
-    _ints(dev, ctx_len=ctx_len, n_new=n_new, dst=dst)
-    _shaped((B,), ctx_len=ctx_len, n_new=n_new)
-    _shaped((B, T), dst=dst)
-    rc = _call_on(dev, svd_cache_write, c, k, v, _dtype_code(k), ks, vs, ctx_len, n_new, dst, B, T,
-                  _on(dev, stream))
-    if rc != SVD_OK:
-        raise SvdError(rc, "svd_cache_write")
+    _call(_c.svd_cache_write, "svd_cache_write", dev, stream, ctypes.addressof(c), k.data_ptr(),
+          v.data_ptr(), _dtype_code(k), ks, vs, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
+          _ptr(n_new, "n_new", dev, i32, (B,)), _ptr(dst, "dst", dev, i32, (B, T)), B, T)
 
 
 def cache_read(cache, block_table, n, start=None, count=None, dtype=None, out=None, stream=None):
     """Positions start[b] .. start[b] + n - 1 of every sequence as (k, v), each
     [B,n,kv_heads,D] of dtype (default torch.bfloat16, or torch.float32).  count
     [B] limits a sequence; the rows behind it are left as out = (k, v) has them."""
-    import torch
-    dev = cache["k"].device
+    torch = _torch()
+    i32 = torch.int32
     B = block_table.shape[0]
-    c = _cache_struct(cache, block_table, B)
-    _ints(dev, start=start, count=count)
-    _shaped((B,), start=start, count=count)
+    c, dev = _cache_struct(cache, block_table, B)
     shape = (B, n, c.kv_heads, c.head_dim)
     if out is None:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        out = tuple(torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
-    k, v = out
-    for t, name in ((k, "out k"), (v, "out v")):
-        _check(t, name, dev)
-    if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
-        raise TypeError("out k and v must share the asked dtype")
-    _shaped(shape, k=k, v=v)
-    rc = _call_on(dev, svd_cache_read, c, start, count, B, n, _dtype_code(k), k, v,
-                  _on(dev, stream))
-    if rc != SVD_OK:
-        raise SvdError(rc, "svd_cache_read")
+        both = torch.empty((2,) + shape, dtype=torch.bfloat16 if dtype is None else dtype,
+                           device=dev)
+        k, v = both.unbind()
+    else:
+        k, v = out
+        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+            raise TypeError("out k and v must share the asked dtype")
+    _call(_c.svd_cache_read, "svd_cache_read", dev, stream, ctypes.addressof(c),
+          _ptr(start, "start", dev, i32, (B,)), _ptr(count, "count", dev, i32, (B,)), B, n,
+          _dtype_code(k), _ptr(k, "out k", dev, k.dtype, shape),
+          _ptr(v, "out v", dev, k.dtype, shape))
     return k, v
 
 
 def tree_attention_workspace(B, T, q_heads, cache, block_table):
     """A workspace for tree_attention calls of these sizes."""
-    import torch
+    torch = _torch()
     k = cache["k"]
     n = svd_tree_attention_workspace_bytes(B, T, q_heads, k.shape[1], k.shape[3],
                                            block_table.shape[1] * k.shape[2])
@@ -890,38 +901,31 @@ def tree_attention(q, cache, block_table, ctx_len, anc=None, n_nodes=None, scale
     positions ctx_len[b] + node.  scale: default D ** -0.5.  Returns out
     [B,T,q_heads,D] bf16 and, when asked for or given, lse [B,T,q_heads] fp32; rows
     from n_nodes[b] on are left as out and lse have them."""
-    import torch
-    dev = cache["k"].device
-    if q.dtype != torch.bfloat16:
+    torch = _torch()
+    i32, bf16 = torch.int32, torch.bfloat16
+    if q.dtype != bf16:
         raise TypeError("q must be bfloat16, got %s" % q.dtype)
     if q.dim() != 4:
         raise ValueError("q must be [B,T,q_heads,D]")
     B, T, Hq, D = q.shape
-    c = _cache_struct(cache, block_table, B)
-    qs = _token_stride(q, "q", Hq, c.head_dim, dev)
+    c, dev = _cache_struct(cache, block_table, B)
+    qs = _tokens(q, "q", Hq, c.head_dim, dev)
     if Hq % c.kv_heads != 0:
         raise ValueError("q_heads must be a multiple of the cache's kv_heads")
-    _ints(dev, ctx_len=ctx_len, anc=anc, n_nodes=n_nodes)
-    _shaped((B,), ctx_len=ctx_len, n_nodes=n_nodes)
-    _shaped((B, T, (T + 31) // 32), anc=anc)
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((B, T, Hq, D), dtype=bf16, device=dev)
     if lse is None and want_lse:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
-    for t, name, dt in ((out, "out", torch.bfloat16), (lse, "lse", torch.float32)):
-        if t is not None:
-            _check(t, name, dev)
-            if t.dtype != dt:
-                raise TypeError("%s must be %s" % (name, dt))
-    _shaped((B, T, Hq, D), out=out)
-    _shaped((B, T, Hq), lse=lse)
     if workspace is None:
         workspace = tree_attention_workspace(B, T, Hq, cache, block_table)
-    rc = _call_on(dev, svd_tree_attention, c, q, qs, ctx_len, n_nodes, anc,
-                  D ** -0.5 if scale is None else scale, B, T, Hq, out, lse, workspace,
-                  workspace.numel(), _on(dev, stream))
-    if rc != SVD_OK:
-        raise SvdError(rc, "svd_tree_attention")
+    _call(_c.svd_tree_attention, "svd_tree_attention", dev, stream, ctypes.addressof(c),
+          q.data_ptr(), qs, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
+          _ptr(n_nodes, "n_nodes", dev, i32, (B,)),
+          _ptr(anc, "anc", dev, i32, (B, T, (T + 31) // 32)),
+          D ** -0.5 if scale is None else scale, B, T, Hq,
+          _ptr(out, "out", dev, bf16, (B, T, Hq, D)),
+          _ptr(lse, "lse", dev, torch.float32, (B, T, Hq)), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return {"out": out, "lse": lse}
 
 
@@ -935,50 +939,42 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
     tokens int32, values fp32); allow [n,ceil(V/32)] int32 bit masks and
     allow_index [B,T] int32 (negative: none).  out: default a new tensor; logits
     itself for a change in place.  Returns out."""
-    import torch
-    dev = logits.device
-    _check(logits, "logits", dev)
-    code = _dtype_code(logits)
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
     if logits.dim() != 3:
         raise ValueError("logits must be [B,T,V]")
-    B, T, V = logits.shape
-    _ints(dev, history=history, hist_len=hist_len, prompt_len=prompt_len, tokens=tokens, anc=anc,
-          n_rows=n_rows, allow=allow, allow_index=allow_index)
-    if history is not None and (history.dim() != 2 or history.shape[0] != B or hist_len is None):
-        raise ValueError("history must be [B,H], with hist_len")
-    _shaped((B,), hist_len=hist_len, prompt_len=prompt_len, n_rows=n_rows, repetition=repetition,
-            frequency=frequency, presence=presence)
-    _shaped((B, T), tokens=tokens, allow_index=allow_index)
-    _shaped((B, T, (T + 31) // 32), anc=anc)
-    for n, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
-        if t is not None:
-            _check(t, n, dev)
-            if t.dtype != torch.float32:
-                raise TypeError("%s must be float32" % n)
+    dev, dtype, shape = logits.device, logits.dtype, logits.shape
+    z = _ptr(logits, "logits", dev, dtype, shape)
+    B, T, V = shape
+    b, bt = (B,), (B, T)
+    H, h = 0, None
+    if history is not None:
+        if history.dim() != 2 or hist_len is None:
+            raise ValueError("history must be [B,H], with hist_len")
+        H = history.shape[1]
+        h = _ptr(history, "history", dev, i32, (B, H)) if H else None
     off = tok = val = None
+    n_bias = 0
     if bias is not None:
         off, tok, val = bias
-        _ints(dev, bias_offsets=off, bias_tokens=tok)
-        _check(val, "bias values", dev)
-        if val.dtype != torch.float32:
-            raise TypeError("bias values must be float32")
-        _shaped((B + 1,), bias_offsets=off)
-        if tok.dim() != 1 or tok.shape != val.shape:
-            raise ValueError("bias tokens and values must be one length")
+        n_bias = tok.numel()
+        off = _ptr(off, "bias offsets", dev, i32, (B + 1,))
+        tok = _ptr(tok, "bias tokens", dev, i32, (n_bias,))
+        val = _ptr(val, "bias values", dev, f32, (n_bias,))
+    n_masks = 0
     if allow is not None:
-        if allow.dim() != 2 or allow.shape[1] != (V + 31) // 32 or allow_index is None:
+        if allow.dim() != 2 or allow_index is None:
             raise ValueError("allow must be [n,ceil(V/32)], with allow_index")
+        n_masks = allow.shape[0]
+        allow = _ptr(allow, "allow", dev, i32, (n_masks, (V + 31) // 32))
     if out is None:
         out = torch.empty_like(logits)
-    _check(out, "out", dev)
-    _shaped((B, T, V), out=out)
-    if out.dtype != logits.dtype:
-        raise TypeError("out must have the dtype of logits")
-    H = 0 if history is None else history.shape[1]
-    rc = _call_on(dev, svd_adjust_logits, logits, out, code, B, T, V, n_rows,
-                  history if H else None, H, hist_len, prompt_len, tokens, anc, repetition,
-                  frequency, presence, off, tok, val, 0 if tok is None else tok.numel(), allow,
-                  allow_index, 0 if allow is None else allow.shape[0], _on(dev, stream))
-    if rc != SVD_OK:
-        raise SvdError(rc, "svd_adjust_logits")
+    _call(_c.svd_adjust_logits, "svd_adjust_logits", dev, stream, z,
+          _ptr(out, "out", dev, dtype, shape), _dtype_code(logits), B, T, V,
+          _ptr(n_rows, "n_rows", dev, i32, b), h, H, _ptr(hist_len, "hist_len", dev, i32, b),
+          _ptr(prompt_len, "prompt_len", dev, i32, b), _ptr(tokens, "tokens", dev, i32, bt),
+          _ptr(anc, "anc", dev, i32, (B, T, (T + 31) // 32)),
+          _ptr(repetition, "repetition", dev, f32, b), _ptr(frequency, "frequency", dev, f32, b),
+          _ptr(presence, "presence", dev, f32, b), off, tok, val, n_bias, allow,
+          _ptr(allow_index, "allow_index", dev, i32, bt), n_masks)
     return out
