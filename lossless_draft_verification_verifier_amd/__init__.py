@@ -715,8 +715,8 @@ def _torch():
 
 def _bad(t, name, dev, dtype, shape):
     """Say what is wrong with a tensor that failed its check."""
-    if not t.is_cuda or t.device != dev:
-        raise ValueError("%s must be on %s" % (name, dev if dev.type == "cuda" else "the GPU"))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d" % (name, dev))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
@@ -725,23 +725,31 @@ def _bad(t, name, dev, dtype, shape):
 
 
 def _ptr(t, name, dev, dtype, shape):
-    """Address of a contiguous tensor of this device, dtype and shape, or None."""
+    """Address of a contiguous tensor of this device (its index), dtype and shape, or None."""
     if t is None:
         return None
-    if (t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous() or
-            dev.type != "cuda"):
+    if (t.get_device() != dev or t.dtype != dtype or t.shape != shape or
+            not t.is_contiguous()):
         _bad(t, name, dev, dtype, shape)
     return t.data_ptr()
 
 
+def _device_of(t, name):
+    """Index of the GPU that a tensor is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be on the GPU" % name)
+    return dev
+
+
 def _call(f, name, dev, stream, *args):
     """f(*args, stream) with dev as the current device; stream: default the current one."""
-    C = _torch()._C
+    C = _T._C
     if stream is None:
-        stream = C._cuda_getCurrentRawStream(dev.index)
-    elif not isinstance(stream, int):
+        stream = C._cuda_getCurrentRawStream(dev)
+    else:
         stream = _addr(stream)
-    if C._cuda_getDevice() == dev.index:
+    if C._cuda_getDevice() == dev:
         rc = f(*args, stream)
     else:
         with _T.cuda.device(dev):
@@ -757,7 +765,7 @@ def draft_tree(drafts, root=None, n_max=None, stream=None):
     of word i // 32: node i is on the node's path), n_nodes [B] and p_index
     [B,K,gamma+1], the rows of the pool [B * n_max, V] for select_and_verify_rows."""
     torch = _torch()
-    dev, i32 = drafts.device, torch.int32
+    dev, i32 = _device_of(drafts, "drafts"), torch.int32
     if drafts.dim() != 3:
         raise ValueError("drafts must be [B,K,gamma]")
     B, K, G = drafts.shape
@@ -797,10 +805,10 @@ def kv_cache(n_pages, kv_heads, page, head_dim, dtype=None, device="cuda"):
 
 
 def _cache_struct(cache, block_table, B):
-    """(the C struct of a cache and its block table, its device)."""
+    """(the C struct of a cache and its block table, the device's index)."""
     torch = _torch()
     k, v = cache["k"], cache["v"]
-    dev, dtype, shape = k.device, k.dtype, k.shape
+    dev, dtype, shape = _device_of(k, "cache k"), k.dtype, k.shape
     if len(shape) != 4:
         raise ValueError("cache k and v must be [n_pages,kv_heads,page,head_dim]")
     if dtype == torch.float8_e4m3fn:
@@ -822,8 +830,8 @@ def _cache_struct(cache, block_table, B):
 
 def _tokens(t, name, heads, D, dev):
     """Elements between the tokens of t [B,T,heads,D], whose heads are contiguous."""
-    if t.device != dev or not t.is_cuda:
-        raise ValueError("%s must be on %s" % (name, dev if dev.type == "cuda" else "the GPU"))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d" % (name, dev))
     shape = t.shape
     if len(shape) != 4 or shape[2] != heads or shape[3] != D:
         raise ValueError("%s must be [B,T,%d,%d], got %s" % (name, heads, D, list(shape)))
@@ -943,7 +951,7 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
     i32, f32 = torch.int32, torch.float32
     if logits.dim() != 3:
         raise ValueError("logits must be [B,T,V]")
-    dev, dtype, shape = logits.device, logits.dtype, logits.shape
+    dev, dtype, shape = _device_of(logits, "logits"), logits.dtype, logits.shape
     z = _ptr(logits, "logits", dev, dtype, shape)
     B, T, V = shape
     b, bt = (B,), (B, T)

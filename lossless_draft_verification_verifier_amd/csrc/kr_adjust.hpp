@@ -12,12 +12,14 @@
 // vocabulary and counts the history's tokens of that range in LDS: dense
 // integer counters, so a repeated token needs no search and the order of the
 // additions cannot show.  A thread then holds the adjustments of its few
-// vocabulary columns in registers for all rows of the prefix, and the row loop
-// touches memory for logits only.  Path tokens differ from row to row; the few
-// nodes whose token falls into the range are kept as a list, and the columns
-// that hold one look through it row by row.
+// vocabulary columns in registers for all rows of the prefix, as one factor and
+// one summand per token, and the row loop touches memory for logits only, kAdjRows
+// rows at a time.  Path tokens differ from row to row; the few nodes whose token
+// falls into the range are kept as a list, and the columns that hold one look
+// through it row by row.
 #pragma once
 
+#include "kr_cache.hpp"
 #include "svd_device.hpp"
 
 namespace svd {
@@ -25,6 +27,7 @@ namespace svd {
 constexpr int kAdjBlock = 512;
 constexpr int kAdjRange = 8192;      // most vocabulary tokens per workgroup
 constexpr int kAdjRangeMin = 1024;   // a workgroup's range when there are few rows
+constexpr int kAdjRows = 4;          // rows whose loads are in flight together
 constexpr int kAdjPathSmall = 256;   // trees of at most this many nodes keep a short list
 constexpr int kAdjPathMax = 4096;
 constexpr uint32_t kAdjSeen = 1u << 31;   // the token occurs in the history
@@ -61,27 +64,28 @@ struct AdjVec<BF16, false> { using type = vec16_at2; };
 template <>
 struct AdjVec<F32, false> { using type = vec16_at4; };
 
-__device__ __forceinline__ uint16_t adj_bf16(float x) {
-  return __builtin_bit_cast(uint16_t, (__bf16)x);
-}
-
-// element i of a 16-byte vector
+// a vector of one value
 template <typename E>
-__device__ __forceinline__ void adj_set(vec16 &w, int i, float x) {
-  if constexpr (sizeof(typename E::elem) == 4) {
-    w[i] = __float_as_uint(x);
-  } else {
-    const uint32_t h = adj_bf16(x);
-    const uint32_t old = w[i >> 1];
-    w[i >> 1] = (i & 1) ? (old & 0xffffu) | (h << 16) : (old & 0xffff0000u) | h;
-  }
+__device__ __forceinline__ vec16 adj_fill(float x) {
+  const uint32_t u = sizeof(typename E::elem) == 4 ? __float_as_uint(x) : pack_bf16(x, x);
+  return vec16{u, u, u, u};
 }
 
-__device__ __forceinline__ float adj_apply(float z, bool seen, int count, float r, float f,
-                                           float pr) {
-  if (seen) z = z > 0.0f ? z / r : z * r;
-  if (count > 0) z = (z - f * (float)count) - pr;
-  return z;
+// element i of a where bit i of m is set, of b elsewhere
+template <typename E>
+__device__ __forceinline__ vec16 adj_select(uint32_t m, const vec16 &a, const vec16 &b) {
+  vec16 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t k;
+    if constexpr (E::kPerVec == 4) {
+      k = ((m >> j) & 1) ? 0xffffffffu : 0u;
+    } else {
+      k = (((m >> (2 * j)) & 1) ? 0x0000ffffu : 0u) | (((m >> (2 * j + 1)) & 1) ? 0xffff0000u : 0u);
+    }
+    r[j] = (a[j] & k) | (b[j] & ~k);
+  }
+  return r;
 }
 
 // grid: prefix x range x row chunk.  kVec: rows start 16-byte aligned.  In
@@ -133,11 +137,17 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   if (hlen > 0) {
     const int32_t *h = a.history + b * a.hist_stride;
     const int made = a.prompt_len ? a.prompt_len[b] : 0;
-    for (int i = tid; i < hlen; i += kAdjBlock) {
-      const uint32_t v = (uint32_t)(h[i] - v0);
-      if (h[i] >= 0 && v < (uint32_t)nv) {
-        atomicOr(&cnt[v], kAdjSeen);
-        if (i >= made) atomicAdd(&cnt[v], 1u);
+    for (int i0 = tid; i0 < hlen; i0 += 8 * kAdjBlock) {
+      int x[8];  // loads of 8 tokens in flight
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = i0 + k * kAdjBlock < hlen ? h[i0 + k * kAdjBlock] : -1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t v = (uint32_t)(x[k] - v0);
+        if (x[k] >= 0 && v < (uint32_t)nv) {
+          atomicOr(&cnt[v], kAdjSeen);
+          if (i0 + k * kAdjBlock >= made) atomicAdd(&cnt[v], 1u);
+        }
       }
     }
   }
@@ -183,6 +193,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   __syncthreads();
 
   const float r = a.repetition ? a.repetition[b] : 1.0f;
+  const float inv = 1.0f / r;
   const float f = a.frequency ? a.frequency[b] : 0.0f;
   const float pr = a.presence ? a.presence[b] : 0.0f;
   const bool rep = a.repetition != nullptr;
@@ -200,62 +211,88 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     }
     return n;
   };
-  auto adjust = [&](float z, int t, int v, uint32_t c) {
-    int n = (int)(c & kAdjCount);
-    bool seen = (c & kAdjSeen) != 0;
-    if (c & kAdjPath) {
-      const int m = on_path(t, (uint32_t)v);
-      n += m;
-      seen |= m > 0;
-    }
-    z = adj_apply(z, rep && seen, n, r, f, pr);
-    if constexpr (kBias) z += bias[v];
-    return z;
+  // what n counted occurrences and the bias add to token v
+  auto summand = [&](int n, int v) {
+    float x = n > 0 ? -(f * (float)n) - pr : 0.0f;
+    if constexpr (kBias) x += bias[v];
+    return x;
+  };
+  auto scaled = [&](float z, float add) {  // one rounding after the factor's
+    return __builtin_fmaf(z, z > 0.0f ? inv : r, add);
+  };
+  // token v of row t, which some node holds
+  auto adjust_path = [&](float z, int t, int v, uint32_t c) {
+    const int m = on_path(t, (uint32_t)v);
+    const float add = summand((int)(c & kAdjCount) + m, v);
+    return rep && (m > 0 || (c & kAdjSeen)) ? scaled(z, add) : z + add;
+  };
+  // the mask row of row t: nullptr for none; poison: an index behind the last
+  auto mask_row = [&](int t, bool &poison) -> const uint32_t * {
+    const int m = a.allow_index[b * T + t];
+    poison = m >= a.n_masks;
+    return m >= 0 && !poison ? a.allow + (int64_t)m * MW : nullptr;
   };
 
+  constexpr uint32_t kAll = (1u << P) - 1;
   const int ncol = nv / P;
   for (int col = tid; col < ncol; col += kAdjBlock) {
     const int v = col * P;
-    uint32_t c[P];
-    bool touched = false;
+    float add[P];
+    uint32_t seen = 0, mine = 0, paths = 0;  // a bit per token
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      c[i] = cnt[v + i];
-      touched |= c[i] != 0;
-      if constexpr (kBias) touched |= bias[v + i] != 0.0f;
+      const uint32_t c = cnt[v + i];
+      add[i] = summand((int)(c & kAdjCount), v + i);
+      seen |= (uint32_t)(rep && (c & kAdjSeen)) << i;
+      paths |= (uint32_t)((c & kAdjPath) != 0) << i;
+      mine |= (uint32_t)(c != 0 || add[i] != 0.0f) << i;
     }
-    for (int t = t0; t < t1; ++t) {
-      uint32_t ok = (1u << P) - 1;
-      bool poison = false;
-      if (a.allow) {
-        const int m = a.allow_index[b * T + t];
-        if (m >= a.n_masks) poison = true;
-        else if (m >= 0)
-          ok &= a.allow[(int64_t)m * MW + ((v0 + v) >> 5)] >> ((v0 + v) & 31);
-      }
-      if (a.in_place && !touched && !poison && ok == (1u << P) - 1) continue;
-      const int64_t at = (int64_t)t * a.V + v;
-      vec16 w = *reinterpret_cast<const V_ *>(src + at);
-      if (touched) {
-        float x[P];
-        E::unpack(w, x);
+    for (int t = t0; t < t1; t += kAdjRows) {
+      uint32_t ok[kAdjRows];
+      bool poison[kAdjRows], skip[kAdjRows];
+      vec16 w[kAdjRows];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          bool mine = c[i] != 0;
-          if constexpr (kBias) mine |= bias[v + i] != 0.0f;
-          if (mine) adj_set<E>(w, i, adjust(x[i], t, v + i, c[i]));
+      for (int k = 0; k < kAdjRows; ++k) {
+        ok[k] = kAll;
+        poison[k] = false;
+        if (a.allow && t + k < t1) {
+          const uint32_t *m = mask_row(t + k, poison[k]);
+          if (m) ok[k] = (m[(v0 + v) >> 5] >> ((v0 + v) & 31)) & kAll;
         }
       }
-      if (ok != (1u << P) - 1) {
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (!((ok >> i) & 1)) adj_set<E>(w, i, kNegInf);
+      for (int k = 0; k < kAdjRows; ++k) {
+        // in place, a vector that nothing changes is not touched, and one that is
+        // forbidden as a whole is not read
+        skip[k] = t + k >= t1 || (a.in_place && !mine && !poison[k] && ok[k] == kAll);
+        if (!skip[k]) w[k] = *reinterpret_cast<const V_ *>(src + (int64_t)(t + k) * a.V + v);
       }
-      if (poison) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) adj_set<E>(w, i, nan);
+      for (int k = 0; k < kAdjRows; ++k) {
+        if (skip[k]) continue;
+        if (mine) {
+          float x[P];
+          E::unpack(w[k], x);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            float y = ((seen >> i) & 1) ? scaled(x[i], add[i]) : x[i] + add[i];
+            if ((paths >> i) & 1) y = adjust_path(x[i], t + k, v + i, cnt[v + i]);
+            x[i] = y;
+          }
+          vec16 y;
+          if constexpr (P == 4) {
+            y = vec16{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3])};
+          } else {
+            y = vec16{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4 % P], x[5 % P]),
+                      pack_bf16(x[6 % P], x[7 % P])};
+          }
+          w[k] = adj_select<E>(mine, y, w[k]);
+        }
+        if (ok[k] != kAll) w[k] = adj_select<E>(ok[k], w[k], adj_fill<E>(kNegInf));
+        if (poison[k]) w[k] = adj_fill<E>(nan);
+        *reinterpret_cast<V_ *>(dst + (int64_t)(t + k) * a.V + v) = w[k];
       }
-      *reinterpret_cast<V_ *>(dst + at) = w;
     }
   }
   // the elements behind the last whole column
@@ -265,20 +302,19 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     const int64_t at = (int64_t)t * a.V + v;
     bool ok = true, poison = false;
     if (a.allow) {
-      const int m = a.allow_index[b * T + t];
-      if (m >= a.n_masks) poison = true;
-      else if (m >= 0) ok = (a.allow[(int64_t)m * MW + ((v0 + v) >> 5)] >> ((v0 + v) & 31)) & 1u;
+      const uint32_t *m = mask_row(t, poison);
+      if (m) ok = (m[(v0 + v) >> 5] >> ((v0 + v) & 31)) & 1u;
     }
     T_ e = src[at];
-    uint32_t c = cnt[v];
+    const uint32_t c = cnt[v];
     bool mine = c != 0;
     if constexpr (kBias) mine |= bias[v] != 0.0f;
-    float z = adjust(E::at(src, at), t, v, c);
+    float z = adjust_path(E::at(src, at), t, v, c);
     if (!ok) z = kNegInf;
     if (poison) z = nan;
     if (mine || !ok || poison) {
       if constexpr (sizeof(T_) == 4) e = z;
-      else e = adj_bf16(z);
+      else e = (T_)pack_bf16(z, z);
     }
     dst[at] = e;
   }

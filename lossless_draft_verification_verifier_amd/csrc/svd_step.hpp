@@ -338,9 +338,8 @@ int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
   while (a.range > kAdjRangeMin && B * T * (((int64_t)V + a.range - 1) / a.range) < 1024)
     a.range /= 2;
   const int64_t nr = ((int64_t)V + a.range - 1) / a.range;
-  a.row_step = T;
-  while (a.row_step > 8 && B * nr * ((T + a.row_step - 1) / a.row_step) < 2048)
-    a.row_step = (a.row_step + 1) / 2;
+  const int64_t want = std::max<int64_t>(1, 1024 / (B * nr));  // workgroups that fit at once
+  a.row_step = (int)std::max<int64_t>(std::min(T, kAdjRows), (T + want - 1) / want);
   a.n_ranges = (int)nr;
   a.n_chunks = (T + a.row_step - 1) / a.row_step;
   const int64_t blocks = B * nr * a.n_chunks;
