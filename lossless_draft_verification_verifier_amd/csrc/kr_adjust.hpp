@@ -13,10 +13,10 @@
 // integer counters, so a repeated token needs no search and the order of the
 // additions cannot show.  A thread then holds the adjustments of its few
 // vocabulary columns in registers for all rows of the prefix, as one factor and
-// one summand per token, and the row loop touches memory for logits only, kAdjRows
-// rows at a time.  Path tokens differ from row to row; the few nodes whose token
-// falls into the range are kept as a list, and the columns that hold one look
-// through it row by row.
+// one summand per token, and the row loop touches memory for logits only.  Path
+// tokens differ from row to row; the few nodes whose token falls into the range
+// are kept as a list, the row loop passes their tokens through as they are, and
+// a pass over (row, node) pairs sets them afterwards.
 #pragma once
 
 #include "kr_cache.hpp"
@@ -24,10 +24,9 @@
 
 namespace svd {
 
-constexpr int kAdjBlock = 512;
-constexpr int kAdjRange = 8192;      // most vocabulary tokens per workgroup
+constexpr int kAdjBlock = 256;
+constexpr int kAdjRange = 4096;      // most vocabulary tokens per workgroup
 constexpr int kAdjRangeMin = 1024;   // a workgroup's range when there are few rows
-constexpr int kAdjRows = 4;          // rows whose loads are in flight together
 constexpr int kAdjPathSmall = 256;   // trees of at most this many nodes keep a short list
 constexpr int kAdjPathMax = 4096;
 constexpr uint32_t kAdjSeen = 1u << 31;   // the token occurs in the history
@@ -99,7 +98,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   constexpr int P = E::kPerVec;
   __shared__ uint32_t cnt[kAdjRange];
   __shared__ float bias[kBias ? kAdjRange : 1];
-  __shared__ uint32_t path[PATH];  // node << 13 | token - v0
+  __shared__ uint32_t path[PATH];  // node << 12 | token - v0; the top bit: an earlier entry has the token
   __shared__ int n_path, dup;
   const int tid = threadIdx.x;
   const int per_b = a.n_ranges * a.n_chunks;
@@ -157,7 +156,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
       const uint32_t v = (uint32_t)(x - v0);
       if (x >= 0 && v < (uint32_t)nv) {
         atomicOr(&cnt[v], kAdjPath);
-        path[atomicAdd(&n_path, 1)] = ((uint32_t)t << 13) | v;
+        path[atomicAdd(&n_path, 1)] = ((uint32_t)t << 12) | v;
       }
     }
   }
@@ -200,17 +199,6 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   const int MW = (a.V + 31) / 32;
   const int np = n_path;
 
-  // how often token v of the range is on row t's path
-  auto on_path = [&](int t, uint32_t v) {
-    int n = 0;
-    for (int i = 0; i < np; ++i) {
-      const uint32_t e = path[i];
-      if ((e & 8191u) != v) continue;
-      const int node = (int)(e >> 13);
-      n += a.anc ? (int)((a.anc[(b * T + t) * W + (node >> 5)] >> (node & 31)) & 1u) : node <= t;
-    }
-    return n;
-  };
   // what n counted occurrences and the bias add to token v
   auto summand = [&](int n, int v) {
     float x = n > 0 ? -(f * (float)n) - pr : 0.0f;
@@ -220,18 +208,18 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   auto scaled = [&](float z, float add) {  // one rounding after the factor's
     return __builtin_fmaf(z, z > 0.0f ? inv : r, add);
   };
-  // token v of row t, which some node holds
-  auto adjust_path = [&](float z, int t, int v, uint32_t c) {
-    const int m = on_path(t, (uint32_t)v);
-    const float add = summand((int)(c & kAdjCount) + m, v);
-    return rep && (m > 0 || (c & kAdjSeen)) ? scaled(z, add) : z + add;
-  };
   // the mask row of row t: nullptr for none; poison: an index behind the last
   auto mask_row = [&](int t, bool &poison) -> const uint32_t * {
     const int m = a.allow_index[b * T + t];
     poison = m >= a.n_masks;
     return m >= 0 && !poison ? a.allow + (int64_t)m * MW : nullptr;
   };
+
+  for (int i = tid; i < np; i += kAdjBlock) {  // order of the list: any, the sums are whole numbers
+    bool again = false;
+    for (int j = 0; j < i; ++j) again |= ((path[j] ^ path[i]) & 4095u) == 0;
+    if (again) atomicOr(&path[i], 0x80000000u);
+  }
 
   constexpr uint32_t kAll = (1u << P) - 1;
   const int ncol = nv / P;
@@ -243,80 +231,84 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     for (int i = 0; i < P; ++i) {
       const uint32_t c = cnt[v + i];
       add[i] = summand((int)(c & kAdjCount), v + i);
+      const uint32_t on = (c & kAdjPath) != 0;
+      paths |= on << i;
       seen |= (uint32_t)(rep && (c & kAdjSeen)) << i;
-      paths |= (uint32_t)((c & kAdjPath) != 0) << i;
-      mine |= (uint32_t)(c != 0 || add[i] != 0.0f) << i;
+      mine |= (uint32_t)(!on && (c != 0 || add[i] != 0.0f)) << i;
     }
-    for (int t = t0; t < t1; t += kAdjRows) {
-      uint32_t ok[kAdjRows];
-      bool poison[kAdjRows], skip[kAdjRows];
-      vec16 w[kAdjRows];
+    for (int t = t0; t < t1; ++t) {
+      uint32_t ok = kAll;
+      bool poison = false;
+      if (a.allow) {
+        const uint32_t *m = mask_row(t, poison);
+        if (m) ok = ((m[(v0 + v) >> 5] >> ((v0 + v) & 31)) | paths) & kAll;
+      }
+      // in place, a vector that nothing changes is not touched
+      if (a.in_place && !mine && !poison && ok == kAll) continue;
+      vec16 w = __builtin_nontemporal_load(
+          reinterpret_cast<const V_ *>(src + (int64_t)t * a.V + v));
+      if (mine) {
+        float x[P];
+        E::unpack(w, x);
 #pragma unroll
-      for (int k = 0; k < kAdjRows; ++k) {
-        ok[k] = kAll;
-        poison[k] = false;
-        if (a.allow && t + k < t1) {
-          const uint32_t *m = mask_row(t + k, poison[k]);
-          if (m) ok[k] = (m[(v0 + v) >> 5] >> ((v0 + v) & 31)) & kAll;
+        for (int i = 0; i < P; ++i)
+          x[i] = ((seen >> i) & 1) ? scaled(x[i], add[i]) : x[i] + add[i];
+        vec16 y;
+        if constexpr (P == 4) {
+          y = vec16{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                    __float_as_uint(x[3])};
+        } else {
+          y = vec16{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4 % P], x[5 % P]),
+                    pack_bf16(x[6 % P], x[7 % P])};
         }
+        w = adj_select<E>(mine, y, w);
       }
-#pragma unroll
-      for (int k = 0; k < kAdjRows; ++k) {
-        // in place, a vector that nothing changes is not touched, and one that is
-        // forbidden as a whole is not read
-        skip[k] = t + k >= t1 || (a.in_place && !mine && !poison[k] && ok[k] == kAll);
-        if (!skip[k]) w[k] = *reinterpret_cast<const V_ *>(src + (int64_t)(t + k) * a.V + v);
-      }
-#pragma unroll
-      for (int k = 0; k < kAdjRows; ++k) {
-        if (skip[k]) continue;
-        if (mine) {
-          float x[P];
-          E::unpack(w[k], x);
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            float y = ((seen >> i) & 1) ? scaled(x[i], add[i]) : x[i] + add[i];
-            if ((paths >> i) & 1) y = adjust_path(x[i], t + k, v + i, cnt[v + i]);
-            x[i] = y;
-          }
-          vec16 y;
-          if constexpr (P == 4) {
-            y = vec16{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3])};
-          } else {
-            y = vec16{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4 % P], x[5 % P]),
-                      pack_bf16(x[6 % P], x[7 % P])};
-          }
-          w[k] = adj_select<E>(mine, y, w[k]);
-        }
-        if (ok[k] != kAll) w[k] = adj_select<E>(ok[k], w[k], adj_fill<E>(kNegInf));
-        if (poison[k]) w[k] = adj_fill<E>(nan);
-        *reinterpret_cast<V_ *>(dst + (int64_t)(t + k) * a.V + v) = w[k];
-      }
+      if (ok != kAll) w = adj_select<E>(ok, w, adj_fill<E>(kNegInf));
+      if (poison) w = adj_select<E>(paths, w, adj_fill<E>(nan));
+      __builtin_nontemporal_store(w, reinterpret_cast<V_ *>(dst + (int64_t)t * a.V + v));
     }
   }
-  // the elements behind the last whole column
+  __syncthreads();
+  // one element from its source value: token v with m nodes of its own on the row's path
+  auto element = [&](int t, int v, int m) {
+    const int64_t at = (int64_t)t * a.V + v;
+    const uint32_t c = cnt[v];
+    bool ok = true, poison = false;
+    if (a.allow) {
+      const uint32_t *row = mask_row(t, poison);
+      if (row) ok = (row[(v0 + v) >> 5] >> ((v0 + v) & 31)) & 1u;
+    }
+    T_ e = src[at];
+    const int n = (int)(c & kAdjCount) + m;
+    const float add = summand(n, v), z = E::at(src, at);
+    float y = rep && (m > 0 || (c & kAdjSeen)) ? scaled(z, add) : z + add;
+    if (!ok) y = kNegInf;
+    if (poison) y = nan;
+    if (m > 0 || (c & ~kAdjPath) != 0 || add != 0.0f || !ok || poison) {
+      if constexpr (sizeof(T_) == 4) e = y;
+      else e = (T_)pack_bf16(y, y);
+    }
+    dst[at] = e;
+  };
+  // tokens that nodes hold, once each: the row loop has left their source values
+  for (int k = tid; k < np * (t1 - t0); k += kAdjBlock) {
+    const int t = t0 + k / np;
+    const uint32_t mine = path[k % np], v = mine & 4095u;
+    if (mine >> 31) continue;
+    int m = 0;
+    for (int i = 0; i < np; ++i) {
+      const uint32_t e = path[i];
+      if ((e & 4095u) != v) continue;
+      const int node = (int)((e & 0x7fffffffu) >> 12);
+      m += a.anc ? (int)((a.anc[(b * T + t) * W + (node >> 5)] >> (node & 31)) & 1u) : node <= t;
+    }
+    element(t, (int)v, m);
+  }
+  // the elements behind the last whole column that no node holds
   const int left = nv - ncol * P;
   for (int i = tid; i < left * (t1 - t0); i += kAdjBlock) {
     const int t = t0 + i / left, v = ncol * P + i % left;
-    const int64_t at = (int64_t)t * a.V + v;
-    bool ok = true, poison = false;
-    if (a.allow) {
-      const uint32_t *m = mask_row(t, poison);
-      if (m) ok = (m[(v0 + v) >> 5] >> ((v0 + v) & 31)) & 1u;
-    }
-    T_ e = src[at];
-    const uint32_t c = cnt[v];
-    bool mine = c != 0;
-    if constexpr (kBias) mine |= bias[v] != 0.0f;
-    float z = adjust_path(E::at(src, at), t, v, c);
-    if (!ok) z = kNegInf;
-    if (poison) z = nan;
-    if (mine || !ok || poison) {
-      if constexpr (sizeof(T_) == 4) e = z;
-      else e = (T_)pack_bf16(z, z);
-    }
-    dst[at] = e;
+    if (!(cnt[v] & kAdjPath)) element(t, v, 0);
   }
 }
 
