@@ -27,6 +27,7 @@ namespace svd {
 constexpr int kAdjBlock = 256;
 constexpr int kAdjRange = 4096;      // most vocabulary tokens per workgroup
 constexpr int kAdjRangeMin = 1024;   // a workgroup's range when there are few rows
+constexpr int kAdjRowsMax = 256;     // most rows per workgroup
 constexpr int kAdjPathSmall = 256;   // trees of at most this many nodes keep a short list
 constexpr int kAdjPathMax = 4096;
 constexpr uint32_t kAdjSeen = 1u << 31;   // the token occurs in the history
@@ -99,6 +100,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   __shared__ uint32_t cnt[kAdjRange];
   __shared__ float bias[kBias ? kAdjRange : 1];
   __shared__ uint32_t path[PATH];  // node << 12 | token - v0; the top bit: an earlier entry has the token
+  __shared__ int row_mask[kAdjRowsMax];  // the rows' masks: -1 for none, n_masks for a bad index
   __shared__ int n_path, dup;
   const int tid = threadIdx.x;
   const int per_b = a.n_ranges * a.n_chunks;
@@ -131,6 +133,9 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     cnt[i] = 0;
     if constexpr (kBias) bias[i] = 0.0f;
   }
+  if (a.allow)
+    for (int i = tid; i < t1 - t0; i += kAdjBlock)
+      row_mask[i] = min(max(a.allow_index[b * T + t0 + i], -1), a.n_masks);
   if (tid == 0) n_path = dup = 0;
   __syncthreads();
   if (hlen > 0) {
@@ -208,9 +213,9 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   auto scaled = [&](float z, float add) {  // one rounding after the factor's
     return __builtin_fmaf(z, z > 0.0f ? inv : r, add);
   };
-  // the mask row of row t: nullptr for none; poison: an index behind the last
+  // the mask of row t, the same for all lanes: nullptr for none; poison: an index behind the last
   auto mask_row = [&](int t, bool &poison) -> const uint32_t * {
-    const int m = a.allow_index[b * T + t];
+    const int m = __builtin_amdgcn_readfirstlane(row_mask[t - t0]);
     poison = m >= a.n_masks;
     return m >= 0 && !poison ? a.allow + (int64_t)m * MW : nullptr;
   };
@@ -275,8 +280,10 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     const uint32_t c = cnt[v];
     bool ok = true, poison = false;
     if (a.allow) {
-      const uint32_t *row = mask_row(t, poison);
-      if (row) ok = (row[(v0 + v) >> 5] >> ((v0 + v) & 31)) & 1u;
+      const int k = row_mask[t - t0];
+      poison = k >= a.n_masks;
+      if (k >= 0 && !poison)
+        ok = (a.allow[(int64_t)k * MW + ((v0 + v) >> 5)] >> ((v0 + v) & 31)) & 1u;
     }
     T_ e = src[at];
     const int n = (int)(c & kAdjCount) + m;

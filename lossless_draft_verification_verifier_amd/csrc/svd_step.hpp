@@ -340,6 +340,7 @@ int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
   const int64_t nr = ((int64_t)V + a.range - 1) / a.range;
   const int64_t want = std::max<int64_t>(1, 1024 / (B * nr));  // workgroups that fit at once
   a.row_step = (int)std::max<int64_t>(std::min(T, 4), (T + want - 1) / want);
+  a.row_step = std::min(a.row_step, kAdjRowsMax);
   a.n_ranges = (int)nr;
   a.n_chunks = (T + a.row_step - 1) / a.row_step;
   const int64_t blocks = B * nr * a.n_chunks;
