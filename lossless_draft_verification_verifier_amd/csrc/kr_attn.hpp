@@ -622,9 +622,11 @@ __global__ __launch_bounds__(kAttnJoinBlock) void kr_attn_join(AttnArgs a, int H
   // a prefix out of range wrote NaN parts for every row
   if (bt % a.T >= nodes && !attn_bad(a.ctx_len[b], nodes, a.T, a.room)) return;
   float m = kNegInf;
+#pragma unroll 8
   for (int s = 0; s < a.S; ++s) m = fmaxf(m, a.part_ms[2 * (s * a.rows_all + row)]);
   float l = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
   for (int s = 0; s < a.S; ++s) {
     const int64_t pr = s * a.rows_all + row;
     const float ms = a.part_ms[2 * pr], ls = a.part_ms[2 * pr + 1];

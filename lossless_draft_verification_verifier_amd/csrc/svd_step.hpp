@@ -91,10 +91,18 @@ struct AttnPlan {
   int nt, wq, wt, m_tiles, m_rows, S;
 };
 
-constexpr int64_t kAttnTargetGroups = 1024;  // workgroups to aim for: four per CU
-constexpr int kAttnPartTokens = 256;         // a part walks at least this many tokens
+// Parts.  Up to 256 workgroups, one per CU, while that leaves a part no more than
+// kAttnLongPart tiles; longer ones in two rounds (32-row waves, one workgroup per CU)
+// or four (16-row waves, two per CU), which smooth prefixes of different
+// lengths.  Measured over S = 1..64: eight requests with 16000 tokens, 95 us with 4 parts,
+// 208 with 1 and 135 with 32; one with 4000 tokens and 129 nodes, 42 us with 10,
+// 87 with 2 and 62 with 16; four with 30000 and 129 nodes, 381 us with 6, 555 with 2,
+// 449 with 10; 24 with 500 to 5000 and 16 heads, 57 us with 3, 73 with 1, 70 with 8.
+constexpr int64_t kAttnCus = 256;
+constexpr int64_t kAttnLongPart = 64;
+constexpr int64_t kAttnMinPart = 2;   // a part walks at least this many tiles
 
-AttnPlan attn_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int64_t room) {
+AttnPlan attn_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t room) {
   AttnPlan p;
   const int64_t rows = (int64_t)T * (Hq / Hkv);
   p.nt = rows <= 64 ? 1 : 2;
@@ -106,9 +114,14 @@ AttnPlan attn_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int64_t room) 
   const int64_t waves = (rows + unit - 1) / unit;
   p.m_rows = (int)((waves + p.m_tiles - 1) / p.m_tiles) * unit;
   const int64_t base = B * Hkv * p.m_tiles;
-  const int64_t most = std::max<int64_t>(1, room / kAttnPartTokens);
-  const int64_t want = (kAttnTargetGroups + base - 1) / base;
-  p.S = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, kAttnMaxSplits}));
+  const int64_t tk = 8192 / D, tiles = (room + tk - 1) / tk;  // as AttnShape::TK
+  int64_t S = std::max<int64_t>(1, kAttnCus / base);
+  if (tiles / S > kAttnLongPart || (p.nt == 1 && base > kAttnCus)) {
+    const int64_t rounds = p.nt == 1 ? 4 : 2;
+    S = std::max(S, (rounds * kAttnCus + base - 1) / base);
+  }
+  S = std::min<int64_t>({S, tiles / kAttnMinPart, kAttnMaxSplits});
+  p.S = (int)std::max<int64_t>(1, S);
   return p;
 }
 
@@ -117,7 +130,7 @@ bool attn_sizes_ok(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int
     return false;
   if (D != 64 && D != 128) return false;
   if (room < 1 || room >= (int64_t)1 << 31) return false;
-  const AttnPlan p = attn_plan(B, T, Hq, Hkv, room);
+  const AttnPlan p = attn_plan(B, T, Hq, Hkv, D, room);
   const int64_t units = B * Hkv * p.S;
   return units < kGridMax / p.m_tiles - 8;
 }
@@ -239,7 +252,7 @@ int svd_cache_read(const svd_cache_t *cache, const int32_t *start, const int32_t
 size_t svd_tree_attention_workspace_bytes(int64_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
                                           int32_t head_dim, int64_t max_len) {
   if (!attn_sizes_ok(B, T, q_heads, kv_heads, head_dim, max_len)) return 0;
-  const AttnPlan p = attn_plan(B, T, q_heads, kv_heads, max_len);
+  const AttnPlan p = attn_plan(B, T, q_heads, kv_heads, head_dim, max_len);
   if (p.S == 1) return kAlign;
   const int64_t rows = B * T * q_heads;
   return attn_ms_offset(rows, p.S, head_dim) + align_up((size_t)rows * p.S * 2 * sizeof(float));
@@ -264,7 +277,7 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
     return SVD_EINVAL;
   if (workspace_bytes < svd_tree_attention_workspace_bytes(B, T, q_heads, c.Hkv, D, room))
     return SVD_EWORKSPACE;
-  const AttnPlan p = attn_plan(B, T, q_heads, c.Hkv, room);
+  const AttnPlan p = attn_plan(B, T, q_heads, c.Hkv, D, room);
   AttnArgs a;
   a.q = static_cast<const uint16_t *>(q);
   a.q_stride = q_stride;
