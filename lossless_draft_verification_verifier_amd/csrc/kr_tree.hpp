@@ -17,9 +17,10 @@
 
 namespace svd {
 
-constexpr int kTreeBlock = 512;
+constexpr int kTreeBlock = 1024;
 constexpr int kTreeMaxK = 64;
 constexpr int kTreeLdsTokens = 4096;  // drafts of at most this many tokens are staged in LDS
+constexpr int kTreeMaxNodes = 4096;
 
 // bits [lo, hi] of a bitmap that fall into word w
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
@@ -36,6 +37,7 @@ __global__ __launch_bounds__(kTreeBlock) void kr_draft_tree(
     int32_t *__restrict__ p_index) {
   __shared__ int32_t tok[kTreeLdsTokens];
   __shared__ int lcp[kTreeMaxK][kTreeMaxK];
+  __shared__ uint8_t owner[kTreeMaxNodes];  // the draft that owns a node
   __shared__ int len[kTreeMaxK], first[kTreeMaxK], base[kTreeMaxK + 1], par[kTreeMaxK];
   const int64_t b = blockIdx.x;
   const int tid = threadIdx.x;
@@ -98,22 +100,18 @@ __global__ __launch_bounds__(kTreeBlock) void kr_draft_tree(
   const bool fits = base[K] <= T;
   const int n = fits ? base[K] : 0;
   if (tid == 0) n_nodes[b] = fits ? n : -1;
-  // the draft that owns node t (1 <= t < n): the last one whose run starts at or before it
-  // and is not empty
-  auto owner_of = [&](int t) {
-    int lo = 0, hi = K - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (base[mid] <= t) lo = mid; else hi = mid - 1;
+  if (fits)
+    for (int i = tid; i < K * G; i += kTreeBlock) {
+      const int k = i / G, j = i % G;
+      if (j >= first[k] && j < len[k]) owner[base[k] + j - first[k]] = (uint8_t)k;
     }
-    return lo;
-  };
+  __syncthreads();
   for (int t = tid; t < T; t += kTreeBlock) {
     int32_t xt = -1, pt = -1, dt = 0;
     if (t == 0 && n > 0) {
       xt = root ? root[b] : -1;
     } else if (t < n) {
-      const int k = owner_of(t), j = t - base[k] + first[k];
+      const int k = owner[t], j = t - base[k] + first[k];
       xt = x[k * G + j];
       dt = j + 1;
       pt = j == 0 ? 0 : j > first[k] ? t - 1 : base[par[k]] + j - 1 - first[par[k]];
@@ -136,22 +134,28 @@ __global__ __launch_bounds__(kTreeBlock) void kr_draft_tree(
     }
     p_index[b * K * (G + 1) + i] = n > 0 && node >= 0 ? (int32_t)(b * T + node) : -1;
   }
-  for (int i = tid; i < T * W; i += kTreeBlock) {
-    const int t = i / W, w = i % W;
-    uint32_t bits = 0;
-    if (t < n) {
-      bits = w == 0 ? 1u : 0u;
-      if (t > 0) {
-        int k = owner_of(t), hi = t - base[k] + first[k];
-        while (true) {
-          bits |= range_bits(base[k], base[k] + hi - first[k], w);
-          hi = first[k] - 1;
-          if (hi < 0) break;
-          k = par[k];
+  // ancestor words: `ws` neighbouring threads share a node
+  int ws = 1;
+  while (ws < W && ws < 32) ws *= 2;
+  const int w0 = tid & (ws - 1);
+  for (int t = tid / ws; t < T; t += kTreeBlock / ws) {
+    uint32_t *row = anc + (b * T + t) * W;
+    for (int w = w0; w < W; w += ws) {
+      uint32_t bits = 0;
+      if (t < n) {
+        bits = w == 0 ? 1u : 0u;
+        if (t > 0) {
+          int k = owner[t], hi = t - base[k] + first[k];
+          while (true) {
+            bits |= range_bits(base[k], base[k] + hi - first[k], w);
+            hi = first[k] - 1;
+            if (hi < 0) break;
+            k = par[k];
+          }
         }
       }
+      row[w] = bits;
     }
-    anc[b * T * W + i] = bits;
   }
 }
 
