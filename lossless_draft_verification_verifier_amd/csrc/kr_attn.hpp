@@ -359,7 +359,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   };
 
   // the waves that compute: their rows, a loop over the tiles, the parts to LDS
-  auto compute = [&](auto &&begin, auto &&end) {
+  auto compute = [&](auto &&before, auto &&begin, auto &&end) {
   const int wq = wave % WQ, wt = wave / WQ;
   vec16 qf[NT][ST];
   int node[NT];
@@ -384,14 +384,14 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   const int steps = (t_hi - t_lo + PF - 1) / PF * PF;  // as the loading waves take
-  if (t_lo < t_hi) begin();
+  if (t_lo < t_hi) before();
   for (int tile = t_lo; tile < t_lo + steps; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
     const bool last = p0 + TK > ctx;  // holds nodes or the end
     const vec16 *const lk =
         reinterpret_cast<const vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     const unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
-    if constexpr (kRoles) __syncthreads();
+    begin(tile);
     if (active && tile < t_hi) {
 #pragma unroll
       for (int g0 = 0; g0 < TW; g0 += G) {
@@ -509,7 +509,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   int pages[PF];
   if constexpr (kRoles) {
     if (wave < Shape::NC) {
-      compute([] {}, [](int) {});
+      compute([] {}, [](int) { __syncthreads(); }, [](int) {});
     } else if (t_lo < t_hi) {
 #pragma unroll
       for (int k = 0; k < PF; ++k) pages[k] = load_pages(t_lo + k);
@@ -532,17 +532,26 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
     auto bring = [&](int tile) {  // tile to LDS, the one after it on its way
       if (tile < t_hi) store_tile(st[0], tile);
       load_tile(st[0], tile + 1, pages[0]);
-      __syncthreads();
     };
+    // the two waves of a SIMD (w and w + 4) bring the next tile one before and one
+    // after they compute: one's products then run beside the other's exponentials
     compute(
         [&] {
           pages[0] = load_pages(t_lo);
           load_tile(st[0], t_lo, pages[0]);
           bring(t_lo);
+          __syncthreads();
         },
-        [&](int tile) { bring(tile + 1); });
+        [&](int tile) {
+          if (do_k) bring(tile + 1);
+        },
+        [&](int tile) {
+          if (do_v) bring(tile + 1);
+          __syncthreads();
+        });
   }
-  __syncthreads();
+
+  __syncthreads();  // the parts of all waves are there
 
   // one row's 4 elements from d on, its exponent and its sum
   auto put = [&](int R, int d, f32x4 x, float mm, float ll, bool first) {
