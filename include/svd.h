@@ -463,8 +463,9 @@ int svd_cache_read(const svd_cache_t *cache, const int32_t *start, const int32_t
  * were.  Data errors: with a ctx_len, n_nodes or sum of both out of range every row
  * of the prefix is NaN; with a page index out of range every row that attends to
  * a token of that page is.
- * Workspace: svd_tree_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim,
- * max_pages * page) bytes (0 for sizes out of range), 256-byte aligned.
+ * scale must be finite and positive.  Workspace: svd_tree_attention_workspace_bytes(
+ * B, T, q_heads, kv_heads, head_dim, max_pages * page) bytes (0 for sizes out of
+ * range), 256-byte aligned; how the call is split follows from these sizes alone.
  */
 size_t svd_tree_attention_workspace_bytes(int64_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
                                           int32_t head_dim, int64_t max_len);

@@ -17,6 +17,13 @@
 // tokens differ from row to row; the few nodes whose token falls into the range
 // are kept as a list, the row loop passes their tokens through as they are, and
 // a pass over (row, node) pairs sets them afterwards.
+//
+// Workgroups of 256 threads over 4096 tokens keep 8 of them on a CU.  2304 bf16 rows
+// of 152064 (256 prefixes of 9 nodes, histories of 512 to 1024, a quarter of the rows
+// masked): 268 us, 5.3 TB/s, against 334 for 512 threads over 8192 tokens and 288 for a
+// copy of the rows.  516 fp32 rows of 100003 with histories to 32768, 300 biases and a
+// mask on every row: 129 us, 3.2 TB/s; setting up a range (its counts, biases and
+// masks) is what is left there.
 #pragma once
 
 #include "kr_cache.hpp"
