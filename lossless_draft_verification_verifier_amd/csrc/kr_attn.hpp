@@ -179,7 +179,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   static_assert(kRoles || Shape::kBlock == 2 * kAttnLoaders, "half of the waves bring keys, half values");
   __shared__ __align__(16) unsigned char lds[Shape::kLdsBytes];
   __shared__ float lds_ms[WT][M][2];
-  __shared__ int lds_odd;                 // some node of this part has a value that is not finite
+  __shared__ int lds_odd;                 // some value of a tile with nodes is not finite
 
   // units on neighbouring blocks run on different XCDs; the row tiles of one
   // unit, which read the same keys and values, stay on one
@@ -581,16 +581,19 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       attn_row_out<D>(a, row, d, x, mm, ll, first);
     }
   };
-  // what the nodes of this part with values that are not finite add to 4 elements
+  // what the tokens of this part whose values are not finite add to 4 elements
   auto odd_values = [&](int R, int d, f32x4 x, float mm) {
     const int nd = R / a.group;
     const uint16_t *q = a.q + (b * a.T + nd) * a.q_stride +
                         (int64_t)(h * a.group + R % a.group) * D;
-    const int64_t lo = max((int64_t)t_lo * TK, (int64_t)ctx);
+    // from the first tile whose values were looked at: it can begin with context, which
+    // every row attends to
+    const int64_t lo = (int64_t)max(t_lo, ctx / TK) * TK;
     const int64_t hi = min((int64_t)t_hi * TK, (int64_t)total);
     for (int64_t p = lo; p < hi; ++p) {
       const int i = (int)(p - ctx);
-      if (a.anc ? !((a.anc[(b * a.T + nd) * W + (i >> 5)] >> (i & 31)) & 1u) : i > nd) continue;
+      if (i >= 0 && (a.anc ? !((a.anc[(b * a.T + nd) * W + (i >> 5)] >> (i & 31)) & 1u) : i > nd))
+        continue;
       const int64_t row = cache_row(cv, b, p, h);
       if (row < 0) continue;
       float v[4];

@@ -251,3 +251,45 @@ def test_repeated_calls_are_bitwise_equal():
     for _ in range(3):
         b = run(svd, p)
         assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_values_of_the_context_reach_every_row(kind, value):
+    # in a whole tile of context, and in the tile that holds the context's end and the nodes
+    svd = require_gpu()
+    for rows in ((5, 4, 2), (40, 8, 2)):
+        T, Hq, Hkv = rows
+        for back in (1, 3, 150):
+            p = problem(2, T, Hq, Hkv, 128, 16, kind, 200, 210, True, seed=18)
+            for b in range(2):
+                pos = int(p["ctx"][b]) - back
+                pg, pl = int(p["tab"][b, pos // 16]), pos % 16
+                if kind == "bf16":
+                    p["c"]["v"][pg, :, pl, 5:9] = value
+                else:
+                    p["c"]["v"].view(torch.uint8)[pg, :, pl, 5:9] = 0x7F
+            got, lse = run(svd, p)
+            for b in range(2):
+                n = int(p["nodes"][b])
+                bad = ~np.isfinite(got[b, :n])
+                assert bad[..., 5:9].all() and not bad[..., :5].any() and not bad[..., 9:].any()
+                if kind == "bf16" and value == float("inf"):
+                    assert (got[b, :n, :, 5:9] == value).all()
+                assert np.isfinite(lse[b, :n]).all()
+
+
+def test_sequences_that_share_pages():
+    # a common prefix of two sequences is read from the same pages
+    svd = require_gpu()
+    p = problem(2, 6, 4, 2, 64, 16, "e4m3", 100, 100, True, seed=19)
+    p["tab"][1, :4] = p["tab"][0, :4]
+    check(svd, p)
+
+
+@pytest.mark.parametrize("rows", [(1, 16, 1), (9, 8, 2), (33, 8, 2), (70, 8, 2), (129, 8, 1)])
+def test_one_page_of_every_size(rows):
+    svd = require_gpu()
+    T, Hq, Hkv = rows
+    for page in (16, 32, 64, 128, 256, 512, 1024):
+        check(svd, problem(1, T, Hq, Hkv, 64, page, "bf16", page + 1, page + 9, True, seed=page))
