@@ -428,8 +428,8 @@ typedef struct {
  *   k, v   rows [kv_heads][head_dim] of dtype (SVD_F32 or SVD_BF16); token (b, t)
  *          starts at element (b * T + t) * k_stride (v_stride)
  * A position without a page (past max_pages, or a page index outside
- * [0, n_pages)) is not written.  Two tokens of one call with the same position
- * leave it with unspecified contents.
+ * [0, n_pages)) is not written.  Two tokens of one call with the same place in the
+ * same page leave it with unspecified contents.
  */
 int svd_cache_write(const svd_cache_t *cache, const void *k, const void *v, svd_dtype_t dtype,
                     int64_t k_stride, int64_t v_stride, const int32_t *ctx_len,
@@ -479,8 +479,9 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
  * verification call (V = the verifier's vocabulary; T = 1: plain decoding).  Row
  * (b, t) predicts the token after node t; its tokens are the history of prefix b
  * and the nodes on its path (tokens[b][i] for the bits of anc[b][t]; anc NULL: nodes
- * 0..t; tokens NULL: none).  Ids outside [0, V) are ignored.  In this order, in
- * fp32, rounded once:
+ * 0..t; tokens NULL: none).  Ids outside [0, V) are ignored.  In this order, as one
+ * factor (z > 0: the rounded 1 / repetition) and one summand in fp32, then rounded to
+ * the logits' type:
  *   z > 0 ? z / repetition[b] : z * repetition[b]   for a token that occurs;
  *   z - frequency[b] * count - presence[b] * [count > 0], count = occurrences
  *     in history[b][prompt_len[b] ..] (prompt_len nullable: 0) and on the path;
@@ -495,7 +496,8 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
  *           but must not overlap it otherwise
  * Values that nothing applies to are copied as they are.  Data errors: a hist_len
  * or n_rows out of range, or an allow_index >= n_masks, gives NaN rows, which a
- * verification call reports as -1.  No workspace.
+ * verification call reports as -1 (all T rows of the prefix for an n_rows out of
+ * range).  No workspace.
  */
 int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t B, int32_t T,
                       int32_t V, const int32_t *n_rows, const int32_t *history,

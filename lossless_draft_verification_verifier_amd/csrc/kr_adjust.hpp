@@ -120,8 +120,9 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   const int rows_b = a.n_rows ? a.n_rows[b] : T;
   const int hlen = a.history ? a.hist_len[b] : 0;
   // a prefix whose lengths are out of range: NaN rows, which a verification reports as -1
-  const bool bad = rows_b < 0 || rows_b > T || hlen < 0 || hlen > a.hist_stride;
-  const int t1 = min(t0 + a.row_step, bad ? T : rows_b);
+  const bool no_rows = rows_b < 0 || rows_b > T;
+  const bool bad = no_rows || hlen < 0 || hlen > a.hist_stride;
+  const int t1 = min(t0 + a.row_step, no_rows ? T : rows_b);
   if (t0 >= t1) return;
   const T_ *src = logits + b * T * (int64_t)a.V + v0;
   T_ *dst = out + b * T * (int64_t)a.V + v0;

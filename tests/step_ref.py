@@ -149,6 +149,9 @@ def adjust(z, bf16, history=None, hist_len=None, prompt_len=None, tokens=None, a
     """z [B,T,V] float64: the adjusted rows and the bound of their errors."""
     B, T, V = z.shape
     out, size = z.copy(), np.abs(z)
+    # 1 / r, f * count, the two sums, then the factor and the summand at once: five
+    # roundings of values no larger than `size`, and one for each bias entry of a token
+    roundings = np.full(z.shape, 5.0)
     for b in range(B):
         for t in range(T):
             toks, made = [], []
@@ -179,11 +182,10 @@ def adjust(z, bf16, history=None, hist_len=None, prompt_len=None, tokens=None, a
                     if 0 <= v < V:
                         row[v] += float(bias[2][i])
                         mag[v] += abs(float(bias[2][i]))
+                        roundings[b, t, v] += 1
             if allow is not None and allow_index[b, t] >= 0:
                 row[~bits(allow[allow_index[b, t]], V)] = -np.inf
-    # a quotient or product, f * count, two differences, the biases: eight roundings of
-    # values no larger than `size`, then the output's own
-    tol = 8 * F32 * size
+    tol = roundings * F32 * size
     if bf16:
         tol = tol + BF16 * (np.where(np.isfinite(out), np.abs(out), 0.0) + tol)
     return out, tol

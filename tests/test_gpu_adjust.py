@@ -1,5 +1,5 @@
 """Penalties, biases and grammar masks against float64, token by token.
-Tolerances: step_ref.adjust derives them (eight fp32 roundings, the output's own)."""
+Tolerances: step_ref.adjust derives them (fp32 roundings, counted, and the output's own)."""
 import numpy as np
 import pytest
 import torch
@@ -191,6 +191,18 @@ def test_data_errors_give_nan_rows():
     nan = torch.isnan(got)
     assert torch.equal(got[0], base[0]) and nan[1].all() and nan[2].all() and nan[4].all()
     assert nan[3, 1].all() and torch.equal(got[3, 0], base[3, 0]) and torch.equal(got[3, 2], base[3, 2])
+
+
+def test_a_bad_history_leaves_the_rows_behind_n_rows():
+    svd = require_gpu()
+    z = torch.randn(2, 4, 100, device="cuda")
+    h = torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+    n = torch.tensor([2, 3], dtype=torch.int32, device="cuda")
+    out = torch.full_like(z, 7.0)
+    svd.adjust_logits(z, history=h, hist_len=torch.tensor([6, 0], dtype=torch.int32, device="cuda"),
+                      n_rows=n, out=out)
+    assert torch.isnan(out[0, :2]).all() and (out[0, 2:] == 7.0).all()
+    assert torch.equal(out[1, :3], z[1, :3]) and (out[1, 3:] == 7.0).all()
 
 
 def test_rows_past_32_bits():
