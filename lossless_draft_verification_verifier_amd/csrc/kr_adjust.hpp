@@ -209,7 +209,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   const float f = a.frequency ? a.frequency[b] : 0.0f;
   const float pr = a.presence ? a.presence[b] : 0.0f;
   const bool rep = a.repetition != nullptr;
-  const int MW = (a.V + 31) / 32;
+  const int MW = (int)(((int64_t)a.V + 31) / 32);  // V goes up to 2^31 - 1
   const int np = n_path;
 
   // what n counted occurrences and the bias add to token v
