@@ -202,7 +202,8 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   const int W = (a.T + 31) / 32;
   const float nan = __uint_as_float(0x7fc00000u);
   const int total = bad ? 0 : ctx + nodes;
-  const int all_tiles = (total + TK - 1) / TK;
+  // a sequence's room goes up to 2^31 - page: sums past its length are 64 bits
+  const int all_tiles = (int)(((int64_t)total + TK - 1) / TK);
   const int per = (all_tiles + a.S - 1) / a.S;
   const int t_lo = s * per, t_hi = min(t_lo + per, all_tiles);
 
@@ -216,7 +217,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // the table's entry for 16-token block `lane` of a tile.  It is looked at when the
   // tile is loaded, not here: that would wait for it
   const int32_t *table = a.table + b * cv.max_pages;
-  const int blocks = (total + 15) / 16;
+  const int blocks = (int)(((int64_t)total + 15) / 16);
   auto load_pages = [&](int tile) -> int {
     const int blk = tile * (TK / 16) + lane % (TK / 16);
     return table[min(blk, blocks - 1) >> (cv.page_shift - 4)];
