@@ -734,6 +734,15 @@ def _ptr(t, name, dev, dtype, shape):
     return t.data_ptr()
 
 
+def _workspace(t, dev):
+    """(address, bytes) of a caller's workspace on this device (its index)."""
+    if t.get_device() != dev:
+        raise ValueError("workspace must be on cuda:%d" % dev)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _device_of(t, name):
     """Index of the GPU that a tensor is on."""
     dev = t.get_device()
@@ -926,14 +935,14 @@ def tree_attention(q, cache, block_table, ctx_len, anc=None, n_nodes=None, scale
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = tree_attention_workspace(B, T, Hq, cache, block_table)
+    ws, ws_bytes = _workspace(workspace, dev)
     _call(_c.svd_tree_attention, "svd_tree_attention", dev, stream, ctypes.addressof(c),
           q.data_ptr(), qs, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
           _ptr(n_nodes, "n_nodes", dev, i32, (B,)),
           _ptr(anc, "anc", dev, i32, (B, T, (T + 31) // 32)),
           D ** -0.5 if scale is None else scale, B, T, Hq,
           _ptr(out, "out", dev, bf16, (B, T, Hq, D)),
-          _ptr(lse, "lse", dev, torch.float32, (B, T, Hq)), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          _ptr(lse, "lse", dev, torch.float32, (B, T, Hq)), ws, ws_bytes)
     return {"out": out, "lse": lse}
 
 
