@@ -427,6 +427,7 @@ def select_and_verify(p, q, drafts, temp_p=1.0, temp_q=None, seed=0, row_base=0,
         "beta": torch.empty((B, K, G), dtype=torch.float32, device=dev) if want_beta else None,
     }
     ws = alloc_workspace(B, K, G, V, dev) if workspace is None else workspace
+    _check(ws, "workspace", dev)
     st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
     rc = svd_select_and_verify(p, q, drafts, _dtype_code(p), B, K, G, V, temp_p, temp_q, seed,
                                row_base, out["selected"], out["accept_len"], out["next_token"],
@@ -459,6 +460,7 @@ def verify(p, q, draft, temp_p=1.0, temp_q=None, seed=0, row_base=0, want_alpha=
         "beta": torch.empty((B, G), dtype=torch.float32, device=dev) if want_beta else None,
     }
     ws = alloc_workspace(B, 1, G, V, dev) if workspace is None else workspace
+    _check(ws, "workspace", dev)
     st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
     rc = svd_verify(p, q, draft, _dtype_code(p), B, G, V, temp_p, temp_q, seed, row_base,
                     out["accept_len"], out["next_token"], out["alpha"], out["beta"], ws,
@@ -491,6 +493,7 @@ def greedy_select_and_verify(p, drafts, temp_p=1.0, seed=0, row_base=0, want_alp
         "alpha": torch.empty((B, K, G), dtype=torch.float32, device=dev) if want_alpha else None,
     }
     ws = alloc_workspace(B, K, G, V, dev) if workspace is None else workspace
+    _check(ws, "workspace", dev)
     st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
     rc = svd_greedy_select_and_verify(p, drafts, _dtype_code(p), B, K, G, V, temp_p, seed,
                                       row_base, out["selected"], out["accept_len"],
@@ -520,6 +523,7 @@ def greedy_verify(p, draft, temp_p=1.0, seed=0, row_base=0, want_alpha=False, wo
         "alpha": torch.empty((B, G), dtype=torch.float32, device=dev) if want_alpha else None,
     }
     ws = alloc_workspace(B, 1, G, V, dev) if workspace is None else workspace
+    _check(ws, "workspace", dev)
     st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
     rc = svd_greedy_verify(p, draft, _dtype_code(p), B, G, V, temp_p, seed, row_base,
                            out["accept_len"], out["next_token"], out["alpha"], ws, ws.numel(), st)
@@ -568,6 +572,7 @@ def select_and_verify_rows(p_pool, p_index, q_pool, q_index, drafts, rule="stand
         if n == 0:
             raise ValueError("sizes out of range")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", dev)
     st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
     temp_q = temp_p if temp_q is None else temp_q
     rc = svd_select_and_verify_rows(
@@ -608,6 +613,7 @@ def verify_window(p, q, drafts, gamma_b=None, eos=-1, rule="standard", early_exi
         "alpha": torch.empty((B, K, G), dtype=torch.float32, device=dev) if want_alpha else None,
     }
     ws = alloc_workspace(B, K, G, V, dev) if workspace is None else workspace
+    _check(ws, "workspace", dev)
     st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
     temp_q = temp_p if temp_q is None else temp_q
     rc = svd_verify_window(SVD_RULE_GREEDY if greedy else SVD_RULE_STANDARD, p,
