@@ -719,6 +719,24 @@ def _torch():
     return _T
 
 
+def _on(stream, t, f, *args):
+    """f(*args) on `stream` (its handle, an int) of t's device.  What f allocates has to
+    belong to that stream: memory of the current one may still be in use there, and goes
+    back to it when its tensor is dropped, while the call still runs.  The results are
+    marked as used on the current stream as well, which is where the caller drops them."""
+    torch = _torch()
+    dev = t.get_device()
+    if dev < 0 or stream == torch._C._cuda_getCurrentRawStream(dev):
+        return f(*args)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+        r = f(*args)
+    for x in r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else (r,):
+        if x is not None:
+            x.record_stream(here)
+    return r
+
+
 def _bad(t, name, dev, dtype, shape):
     """Say what is wrong with a tensor that failed its check."""
     if t.get_device() != dev:
@@ -757,13 +775,10 @@ def _device_of(t, name):
     return dev
 
 
-def _call(f, name, dev, stream, *args):
-    """f(*args, stream) with dev as the current device; stream: default the current one."""
+def _call(f, name, dev, *args):
+    """f(*args, the current stream) with dev as the current device."""
     C = _T._C
-    if stream is None:
-        stream = C._cuda_getCurrentRawStream(dev)
-    else:
-        stream = _addr(stream)
+    stream = C._cuda_getCurrentRawStream(dev)
     if C._cuda_getDevice() == dev:
         rc = f(*args, stream)
     else:
@@ -779,6 +794,8 @@ def draft_tree(drafts, root=None, n_max=None, stream=None):
     suffices).  Returns tokens, parent, depth [B,n_max], anc [B,n_max,W] (bit i % 32
     of word i // 32: node i is on the node's path), n_nodes [B] and p_index
     [B,K,gamma+1], the rows of the pool [B * n_max, V] for select_and_verify_rows."""
+    if stream is not None:
+        return _on(stream, drafts, draft_tree, drafts, root, n_max)
     torch = _torch()
     dev, i32 = _device_of(drafts, "drafts"), torch.int32
     if drafts.dim() != 3:
@@ -795,7 +812,7 @@ def draft_tree(drafts, root=None, n_max=None, stream=None):
     o5 = o4 + B * P
     flat = torch.empty(max(o5 + B, 0), dtype=i32, device=dev)
     at = flat.data_ptr()
-    _call(_c.svd_draft_tree, "svd_draft_tree", dev, stream, d, r, B, K, G, T, at, at + 4 * o1,
+    _call(_c.svd_draft_tree, "svd_draft_tree", dev, d, r, B, K, G, T, at, at + 4 * o1,
           at + 4 * o2, at + 4 * o3, at + 4 * o5, at + 4 * o4)
     view = flat.as_strided
     return {"tokens": view((B, T), (T, 1)), "parent": view((B, T), (T, 1), o1),
@@ -868,6 +885,8 @@ def cache_write(cache, k, v, block_table, ctx_len, n_new=None, dst=None, stream=
     a fused projection) to positions ctx_len[b] + t, or ctx_len[b] + dst[b,t] where
     dst is not negative; n_new [B] limits the tokens of a sequence.  cache: as from
     kv_cache; block_table [B,max_pages], ctx_len [B], dst [B,T] int32."""
+    if stream is not None:
+        return _on(stream, k, cache_write, cache, k, v, block_table, ctx_len, n_new, dst)
     i32 = _torch().int32
     B, T = k.shape[:2]
     c, dev = _cache_struct(cache, block_table, B)
@@ -875,7 +894,7 @@ def cache_write(cache, k, v, block_table, ctx_len, n_new=None, dst=None, stream=
     vs = _tokens(v, "v", c.kv_heads, c.head_dim, dev)
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must share one shape and dtype")
-    _call(_c.svd_cache_write, "svd_cache_write", dev, stream, ctypes.addressof(c), k.data_ptr(),
+    _call(_c.svd_cache_write, "svd_cache_write", dev, ctypes.addressof(c), k.data_ptr(),
           v.data_ptr(), _dtype_code(k), ks, vs, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
           _ptr(n_new, "n_new", dev, i32, (B,)), _ptr(dst, "dst", dev, i32, (B, T)), B, T)
 
@@ -884,6 +903,8 @@ def cache_read(cache, block_table, n, start=None, count=None, dtype=None, out=No
     """Positions start[b] .. start[b] + n - 1 of every sequence as (k, v), each
     [B,n,kv_heads,D] of dtype (default torch.bfloat16, or torch.float32).  count
     [B] limits a sequence; the rows behind it are left as out = (k, v) has them."""
+    if stream is not None:
+        return _on(stream, block_table, cache_read, cache, block_table, n, start, count, dtype, out)
     torch = _torch()
     i32 = torch.int32
     B = block_table.shape[0]
@@ -897,7 +918,7 @@ def cache_read(cache, block_table, n, start=None, count=None, dtype=None, out=No
         k, v = out
         if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
             raise TypeError("out k and v must share the asked dtype")
-    _call(_c.svd_cache_read, "svd_cache_read", dev, stream, ctypes.addressof(c),
+    _call(_c.svd_cache_read, "svd_cache_read", dev, ctypes.addressof(c),
           _ptr(start, "start", dev, i32, (B,)), _ptr(count, "count", dev, i32, (B,)), B, n,
           _dtype_code(k), _ptr(k, "out k", dev, k.dtype, shape),
           _ptr(v, "out v", dev, k.dtype, shape))
@@ -924,6 +945,9 @@ def tree_attention(q, cache, block_table, ctx_len, anc=None, n_nodes=None, scale
     positions ctx_len[b] + node.  scale: default D ** -0.5.  Returns out
     [B,T,q_heads,D] bf16 and, when asked for or given, lse [B,T,q_heads] fp32; rows
     from n_nodes[b] on are left as out and lse have them."""
+    if stream is not None:
+        return _on(stream, q, tree_attention, q, cache, block_table, ctx_len, anc, n_nodes, scale,
+                   out, lse, want_lse, workspace)
     torch = _torch()
     i32, bf16 = torch.int32, torch.bfloat16
     if q.dtype != bf16:
@@ -942,7 +966,7 @@ def tree_attention(q, cache, block_table, ctx_len, anc=None, n_nodes=None, scale
     if workspace is None:
         workspace = tree_attention_workspace(B, T, Hq, cache, block_table)
     ws, ws_bytes = _workspace(workspace, dev)
-    _call(_c.svd_tree_attention, "svd_tree_attention", dev, stream, ctypes.addressof(c),
+    _call(_c.svd_tree_attention, "svd_tree_attention", dev, ctypes.addressof(c),
           q.data_ptr(), qs, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
           _ptr(n_nodes, "n_nodes", dev, i32, (B,)),
           _ptr(anc, "anc", dev, i32, (B, T, (T + 31) // 32)),
@@ -962,6 +986,9 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
     tokens int32, values fp32); allow [n,ceil(V/32)] int32 bit masks and
     allow_index [B,T] int32 (negative: none).  out: default a new tensor; logits
     itself for a change in place.  Returns out."""
+    if stream is not None:
+        return _on(stream, logits, adjust_logits, logits, history, hist_len, prompt_len, tokens,
+                   anc, n_rows, repetition, frequency, presence, bias, allow, allow_index, out)
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
     if logits.dim() != 3:
@@ -992,7 +1019,7 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
         allow = _ptr(allow, "allow", dev, i32, (n_masks, (V + 31) // 32))
     if out is None:
         out = torch.empty_like(logits)
-    _call(_c.svd_adjust_logits, "svd_adjust_logits", dev, stream, z,
+    _call(_c.svd_adjust_logits, "svd_adjust_logits", dev, z,
           _ptr(out, "out", dev, dtype, shape), _dtype_code(logits), B, T, V,
           _ptr(n_rows, "n_rows", dev, i32, b), h, H, _ptr(hist_len, "hist_len", dev, i32, b),
           _ptr(prompt_len, "prompt_len", dev, i32, b), _ptr(tokens, "tokens", dev, i32, bt),
