@@ -369,6 +369,35 @@ svd_strerror = _default.svd_strerror
 # --------------------------------------------------------------------------
 # Tensor conveniences
 
+_T = None  # torch, once a convenience has been called
+
+
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
+
+
+def _on(stream, t, f, *args):
+    """f(*args) on `stream` (its handle, an int) of t's device.  What f allocates has to
+    belong to that stream: memory of the current one may still be in use there, and goes
+    back to it when its tensor is dropped, while the call still runs.  The results are
+    marked as used on the current stream as well, which is where the caller drops them."""
+    torch = _torch()
+    dev = t.get_device()
+    if dev < 0 or stream == torch._C._cuda_getCurrentRawStream(dev):
+        return f(*args)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+        r = f(*args)
+    for x in r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else (r,):
+        if x is not None:
+            x.record_stream(here)
+    return r
+
+
 def _dtype_code(t):
     import torch
     if t.dtype == torch.bfloat16:
@@ -402,6 +431,9 @@ def select_and_verify(p, q, drafts, temp_p=1.0, temp_q=None, seed=0, row_base=0,
                       want_alpha=False, want_beta=False, want_scores=False, workspace=None,
                       stream=None):
     """p [B,K,gamma+1,V], q [B,K,gamma,V] (bf16 or fp32), drafts [B,K,gamma] int32."""
+    if stream is not None:
+        return _on(stream, p, select_and_verify, p, q, drafts, temp_p, temp_q, seed, row_base,
+                   want_alpha, want_beta, want_scores, workspace)
     import torch
     dev = p.device
     for t, n in ((p, "p"), (q, "q"), (drafts, "drafts")):
@@ -428,7 +460,7 @@ def select_and_verify(p, q, drafts, temp_p=1.0, temp_q=None, seed=0, row_base=0,
     }
     ws = alloc_workspace(B, K, G, V, dev) if workspace is None else workspace
     _check(ws, "workspace", dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     rc = svd_select_and_verify(p, q, drafts, _dtype_code(p), B, K, G, V, temp_p, temp_q, seed,
                                row_base, out["selected"], out["accept_len"], out["next_token"],
                                out["scores"], out["alpha"], out["beta"], ws, ws.numel(), st)
@@ -440,6 +472,9 @@ def select_and_verify(p, q, drafts, temp_p=1.0, temp_q=None, seed=0, row_base=0,
 def verify(p, q, draft, temp_p=1.0, temp_q=None, seed=0, row_base=0, want_alpha=False,
            want_beta=False, workspace=None, stream=None):
     """p [B,gamma+1,V], q [B,gamma,V] (bf16 or fp32), draft [B,gamma] int32."""
+    if stream is not None:
+        return _on(stream, p, verify, p, q, draft, temp_p, temp_q, seed, row_base, want_alpha,
+                   want_beta, workspace)
     import torch
     dev = p.device
     for t, n in ((p, "p"), (q, "q"), (draft, "draft")):
@@ -461,7 +496,7 @@ def verify(p, q, draft, temp_p=1.0, temp_q=None, seed=0, row_base=0, want_alpha=
     }
     ws = alloc_workspace(B, 1, G, V, dev) if workspace is None else workspace
     _check(ws, "workspace", dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     rc = svd_verify(p, q, draft, _dtype_code(p), B, G, V, temp_p, temp_q, seed, row_base,
                     out["accept_len"], out["next_token"], out["alpha"], out["beta"], ws,
                     ws.numel(), st)
@@ -473,6 +508,9 @@ def verify(p, q, draft, temp_p=1.0, temp_q=None, seed=0, row_base=0, want_alpha=
 def greedy_select_and_verify(p, drafts, temp_p=1.0, seed=0, row_base=0, want_alpha=False,
                              want_scores=False, workspace=None, stream=None):
     """Greedy acceptance: p [B,K,gamma+1,V] (bf16 or fp32), drafts [B,K,gamma] int32."""
+    if stream is not None:
+        return _on(stream, p, greedy_select_and_verify, p, drafts, temp_p, seed, row_base,
+                   want_alpha, want_scores, workspace)
     import torch
     dev = p.device
     for t, n in ((p, "p"), (drafts, "drafts")):
@@ -494,7 +532,7 @@ def greedy_select_and_verify(p, drafts, temp_p=1.0, seed=0, row_base=0, want_alp
     }
     ws = alloc_workspace(B, K, G, V, dev) if workspace is None else workspace
     _check(ws, "workspace", dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     rc = svd_greedy_select_and_verify(p, drafts, _dtype_code(p), B, K, G, V, temp_p, seed,
                                       row_base, out["selected"], out["accept_len"],
                                       out["next_token"], out["scores"], out["alpha"], ws,
@@ -507,6 +545,9 @@ def greedy_select_and_verify(p, drafts, temp_p=1.0, seed=0, row_base=0, want_alp
 def greedy_verify(p, draft, temp_p=1.0, seed=0, row_base=0, want_alpha=False, workspace=None,
                   stream=None):
     """Greedy acceptance, one draft: p [B,gamma+1,V] (bf16 or fp32), draft [B,gamma] int32."""
+    if stream is not None:
+        return _on(stream, p, greedy_verify, p, draft, temp_p, seed, row_base, want_alpha,
+                   workspace)
     import torch
     dev = p.device
     for t, n in ((p, "p"), (draft, "draft")):
@@ -524,7 +565,7 @@ def greedy_verify(p, draft, temp_p=1.0, seed=0, row_base=0, want_alpha=False, wo
     }
     ws = alloc_workspace(B, 1, G, V, dev) if workspace is None else workspace
     _check(ws, "workspace", dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     rc = svd_greedy_verify(p, draft, _dtype_code(p), B, G, V, temp_p, seed, row_base,
                            out["accept_len"], out["next_token"], out["alpha"], ws, ws.numel(), st)
     if rc != SVD_OK:
@@ -537,6 +578,9 @@ def select_and_verify_rows(p_pool, p_index, q_pool, q_index, drafts, rule="stand
                            workspace=None, stream=None):
     """Shared rows: p_pool [NP,V], p_index [B,K,gamma+1] int32, q_pool [NQ,V] and
     q_index [B,K,gamma] int32 (None for rule="greedy"), drafts [B,K,gamma] int32."""
+    if stream is not None:
+        return _on(stream, p_pool, select_and_verify_rows, p_pool, p_index, q_pool, q_index, drafts,
+                   rule, temp_p, temp_q, seed, row_base, want_alpha, want_scores, workspace)
     import torch
     greedy = rule == "greedy"
     if rule not in ("standard", "greedy"):
@@ -573,7 +617,7 @@ def select_and_verify_rows(p_pool, p_index, q_pool, q_index, drafts, rule="stand
             raise ValueError("sizes out of range")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     _check(workspace, "workspace", dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     temp_q = temp_p if temp_q is None else temp_q
     rc = svd_select_and_verify_rows(
         SVD_RULE_GREEDY if greedy else SVD_RULE_STANDARD, p_pool, NP, p_index,
@@ -591,6 +635,9 @@ def verify_window(p, q, drafts, gamma_b=None, eos=-1, rule="standard", early_exi
     """Ragged, EOS-aware windows: p [B,K,gamma+1,V], q [B,K,gamma,V] (None for
     rule="greedy"), drafts [B,K,gamma] int32, gamma_b [B] int32 or None, eos a token or -1.
     early_exit (K = 1): stream positions only up to each prefix's first rejection."""
+    if stream is not None:
+        return _on(stream, p, verify_window, p, q, drafts, gamma_b, eos, rule, early_exit, temp_p,
+                   temp_q, seed, row_base, want_alpha, want_scores, workspace)
     import torch
     greedy = rule == "greedy"
     if rule not in ("standard", "greedy"):
@@ -614,7 +661,7 @@ def verify_window(p, q, drafts, gamma_b=None, eos=-1, rule="standard", early_exi
     }
     ws = alloc_workspace(B, K, G, V, dev) if workspace is None else workspace
     _check(ws, "workspace", dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     temp_q = temp_p if temp_q is None else temp_q
     rc = svd_verify_window(SVD_RULE_GREEDY if greedy else SVD_RULE_STANDARD, p,
                            None if greedy else q, drafts, gamma_b, eos, int(bool(early_exit)),
@@ -629,6 +676,8 @@ def verify_window(p, q, drafts, gamma_b=None, eos=-1, rule="standard", early_exi
 def cps_lattice(q, temp_q=1.0, tau=0.8, m_max=15, eos=-1, stream=None, lib=None):
     """Candidate lattice of drafter logits q [B, G, V] (bf16 or fp32); lib: the
     Library to call (default: the product library)."""
+    if stream is not None:
+        return _on(stream, q, cps_lattice, q, temp_q, tau, m_max, eos, None, lib)
     import torch
     dev = q.device
     _check(q, "q", dev)
@@ -641,7 +690,7 @@ def cps_lattice(q, temp_q=1.0, tau=0.8, m_max=15, eos=-1, stream=None, lib=None)
     if n == 0:
         raise ValueError("sizes out of range")
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     lib = _default if lib is None else lib
     rc = lib.svd_cps_lattice(q, _dtype_code(q), B, G, V, temp_q, tau, m_max, eos, out["cand"],
                              out["cand_logp"], out["n_cand"], out["len"], ws, n, st)
@@ -653,6 +702,8 @@ def cps_lattice(q, temp_q=1.0, tau=0.8, m_max=15, eos=-1, stream=None, lib=None)
 def cps_beam(lat, fluency=None, lam=1.0, beam=3, stream=None, lib=None):
     """Beam search over a lattice from cps_lattice; fluency [B, G, m_max, m_max] fp32 or None;
     lib: the Library to call (default: the product library)."""
+    if stream is not None:
+        return _on(stream, lat["cand"], cps_beam, lat, fluency, lam, beam, None, lib)
     import torch
     cand = lat["cand"]
     dev = cand.device
@@ -664,7 +715,7 @@ def cps_beam(lat, fluency=None, lam=1.0, beam=3, stream=None, lib=None):
     out = {"paths": torch.empty((B, beam, G), dtype=torch.int32, device=dev),
            "score": torch.empty((B, beam), dtype=torch.float32, device=dev),
            "path_len": torch.empty((B, beam), dtype=torch.int32, device=dev)}
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     lib = _default if lib is None else lib
     rc = lib.svd_cps_beam(cand, lat["cand_logp"], lat["n_cand"], lat["len"], fluency, lam, B, G,
                           M, beam, out["paths"], out["score"], out["path_len"], st)
@@ -679,6 +730,9 @@ def adl_next(drafts, selected, accept_len, avg, gamma_b=None, eos=-1, k_min=1, k
     drafts [B,K,gamma] int32 and selected, accept_len [B] int32 (a verification
     call's inputs and outputs), gamma_b [B] int32 or None, avg [B,2] int32
     updated in place.  Returns next [B] int32."""
+    if stream is not None:
+        return _on(stream, drafts, adl_next, drafts, selected, accept_len, avg, gamma_b, eos, k_min,
+                   k_max, step, shift, slack)
     import torch
     dev = drafts.device
     tens = [(drafts, "drafts"), (selected, "selected"), (accept_len, "accept_len"),
@@ -692,7 +746,7 @@ def adl_next(drafts, selected, accept_len, avg, gamma_b=None, eos=-1, k_min=1, k
             tuple(avg.shape) != (B, 2) or (gamma_b is not None and tuple(gamma_b.shape) != (B,))):
         raise ValueError("selected, accept_len, gamma_b must be [B] and avg [B, 2]")
     nxt = torch.empty(B, dtype=torch.int32, device=dev)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    st = torch.cuda.current_stream(dev).cuda_stream
     rc = svd_adl_next(drafts, selected, accept_len, gamma_b, eos, B, K, G, k_min, k_max, step,
                       shift, slack, avg, nxt, st)
     if rc != SVD_OK:
@@ -707,35 +761,6 @@ def adl_next(drafts, selected, accept_len, avg, gamma_b=None, eos=-1, k_min=1, k
 # A decode step makes these calls on small tensors, where the host's share is
 # what counts: one check per tensor, pointers passed as they are, the current
 # stream's handle taken without a Stream object.
-
-_T = None  # torch, once a convenience has been called
-
-
-def _torch():
-    global _T
-    if _T is None:
-        import torch
-        _T = torch
-    return _T
-
-
-def _on(stream, t, f, *args):
-    """f(*args) on `stream` (its handle, an int) of t's device.  What f allocates has to
-    belong to that stream: memory of the current one may still be in use there, and goes
-    back to it when its tensor is dropped, while the call still runs.  The results are
-    marked as used on the current stream as well, which is where the caller drops them."""
-    torch = _torch()
-    dev = t.get_device()
-    if dev < 0 or stream == torch._C._cuda_getCurrentRawStream(dev):
-        return f(*args)
-    here = torch.cuda.current_stream(dev)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
-        r = f(*args)
-    for x in r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else (r,):
-        if x is not None:
-            x.record_stream(here)
-    return r
-
 
 def _bad(t, name, dev, dtype, shape):
     """Say what is wrong with a tensor that failed its check."""

@@ -48,15 +48,47 @@ def step_calls(svd):
     return [("tree", tree), ("attention", attention), ("read", read), ("adjust", adjust)]
 
 
+def verification_calls(svd):
+    torch.manual_seed(6)
+    B, K, G, V = 3, 2, 4, 20011
+    p = torch.randn(B, K, G + 1, V, device="cuda")
+    q = torch.randn(B, K, G, V, device="cuda")
+    d = torch.randint(0, V, (B, K, G), dtype=torch.int32, device="cuda")
+    p1, q1, d1 = (x[:, 0].contiguous() for x in (p, q, d))
+    px = torch.arange(B * K * (G + 1), dtype=torch.int32, device="cuda").view(B, K, G + 1)
+    qx = torch.arange(B * K * G, dtype=torch.int32, device="cuda").view(B, K, G)
+    pp, qp = p.view(-1, V), q.view(-1, V)
+    lat = svd.cps_lattice(q1)
+    first, length, avg = i32(0, 1, 0), i32(2, 4, 1), torch.zeros((B, 2), dtype=torch.int32, device="cuda")
+
+    def call(f, *a, **fixed):
+        def run(**kw):
+            r = f(*a, **fixed, **kw)
+            return tuple(x for x in (r.values() if isinstance(r, dict) else (r,)) if x is not None)
+        return run
+
+    return [("select", call(svd.select_and_verify, p, q, d, want_alpha=True, want_beta=True)),
+            ("verify", call(svd.verify, p1, q1, d1, want_alpha=True)),
+            ("greedy_select", call(svd.greedy_select_and_verify, p, d, want_alpha=True)),
+            ("greedy", call(svd.greedy_verify, p1, d1)),
+            ("rows", call(svd.select_and_verify_rows, pp, px, qp, qx, d)),
+            ("window", call(svd.verify_window, p, q, d, gamma_b=length)),
+            ("lattice", call(svd.cps_lattice, q1)),
+            ("beam", call(svd.cps_beam, lat)),
+            # shift = 0: the window follows the last step alone, so that every call gives the same
+            ("adl", call(svd.adl_next, d, first, length, avg, shift=0))]
+
+
 def calls(svd):
-    return step_calls(svd)
+    return step_calls(svd) + verification_calls(svd)
 
 
 def storages(r):
     return {x.untyped_storage().data_ptr(): x.untyped_storage().nbytes() for x in r}
 
 
-NAMES = ["tree", "attention", "read", "adjust"]
+NAMES = ["tree", "attention", "read", "adjust", "select", "verify", "greedy_select", "greedy", "rows",
+         "window", "lattice", "beam", "adl"]
 
 
 @pytest.fixture(params=NAMES)
@@ -115,26 +147,26 @@ def test_dropped_results_go_back_after_the_call(job):
         assert (x == 7).all()
 
 
-def test_a_default_workspace_lasts_as_long_as_the_call(monkeypatch):
-    svd = require_gpu()
-    call = dict(calls(svd))["attention"]
+def test_what_a_call_allocates_lasts_as_long_as_the_call(job, monkeypatch):
+    svd, call = job
     want = [x.clone() for x in call()]
-    made, make = [], svd.tree_attention_workspace
+    made, empty = [], torch.empty
 
-    def spy(*a):
-        w = make(*a)
-        made.append((w.data_ptr(), w.numel()))
-        return w
+    def spy(*a, **kw):
+        t = empty(*a, **kw)
+        made.append((t.data_ptr(), max(t.numel() * t.element_size(), 1)))
+        return t
 
-    monkeypatch.setattr(svd, "tree_attention_workspace", spy)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
         torch.cuda._sleep(SPIN)
+    monkeypatch.setattr(torch, "empty", spy)
     got = call(stream=side.cuda_stream)
-    (at, n), = made
-    fill = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(8)]
-    assert all(x.data_ptr() != at for x in fill)
+    monkeypatch.undo()
+    fill = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _, n in made for _ in range(4)]
+    taken = {x.data_ptr() for x in fill}
+    assert not any(at in taken for at, _ in made)
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
