@@ -402,8 +402,8 @@ int svd_draft_tree(const int32_t *drafts, const int32_t *root, int64_t B, int32_
  * values, e in [-126, 120]: k_scale and v_scale [n_pages][kv_heads][page] hold
  * e + 127 (a byte from 1 to 254).  A value is code * 2^e, exactly, in bf16 too (what
  * would round to 2^128 is held as 240 * 2^120); an infinity or NaN is held as NaN.  Limits: head_dim 64 or 128; page a power of
- * two from 16 to 1024; max_pages * page < 2^31; k and v 16-byte aligned.  The
- * struct is read during the call only.
+ * two from 16 to 1024; max_pages * page < 2^31; k and v 16-byte aligned, k_scale
+ * and v_scale 4-byte aligned.  The struct is read during the call only.
  */
 typedef enum {
   SVD_CACHE_BF16 = 0,

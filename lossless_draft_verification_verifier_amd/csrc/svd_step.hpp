@@ -17,6 +17,9 @@ int cache_view(const svd_cache_t *c, CacheView &v) {
   if (c->dtype != SVD_CACHE_BF16 && c->dtype != SVD_CACHE_E4M3) return SVD_EDTYPE;
   const bool e4m3 = c->dtype == SVD_CACHE_E4M3;
   if (e4m3 && (!c->k_scale || !c->v_scale)) return SVD_EINVAL;
+  // the attention reads the scales of four tokens as one word
+  if (e4m3 && (((uintptr_t)c->k_scale) % 4 != 0 || ((uintptr_t)c->v_scale) % 4 != 0))
+    return SVD_EINVAL;
   if (c->head_dim != 64 && c->head_dim != 128) return SVD_EINVAL;
   if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1)) != 0) return SVD_EINVAL;
   if (c->n_pages < 1 || c->n_pages >= (int64_t)1 << 31 || c->max_pages < 1 || c->kv_heads < 1 ||
