@@ -494,7 +494,8 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
  *   n_rows  [B] nullable (T): rows from n_rows[b] on are left as they were
  *   out     [B][T][V]; may be logits itself (only what changes is then moved),
  *           but must not overlap it otherwise
- * Values that nothing applies to are copied as they are.  Data errors: a hist_len
+ * Values that nothing applies to are copied as they are, NaN payloads and signs of
+ * zero included (a repetition of 1 and a summand of 0 are nothing).  Data errors: a hist_len
  * or n_rows out of range, or an allow_index >= n_masks, gives NaN rows, which a
  * verification call reports as -1 (all T rows of the prefix for an n_rows out of
  * range).  No workspace.

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   // counts, path list and biases of the range
   for (int i = tid; i < nv; i += kAdjBlock) {
     cnt[i] = 0;
-    if constexpr (kBias) bias[i] = 0.0f;
+    if constexpr (kBias) bias[i] = 0.0f;  // a count of 0, first
   }
   if (a.allow)
     for (int i = tid; i < t1 - t0; i += kAdjBlock)
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     }
     __syncthreads();
     const bool ordered = dup != 0;
-    for (int i = tid; i < nv; i += kAdjBlock) bias[i] = 0.0f;
+    for (int i = tid; i < nv; i += kAdjBlock) bias[i] = -0.0f;
     __syncthreads();
     if (!ordered) {
       for (int64_t i = lo + tid; i < hi; i += kAdjBlock) {
@@ -208,13 +208,13 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
   const float inv = 1.0f / r;
   const float f = a.frequency ? a.frequency[b] : 0.0f;
   const float pr = a.presence ? a.presence[b] : 0.0f;
-  const bool rep = a.repetition != nullptr;
+  const bool rep = r != 1.0f;
   const int MW = (int)(((int64_t)a.V + 31) / 32);  // V goes up to 2^31 - 1
   const int np = n_path;
 
-  // what n counted occurrences and the bias add to token v
+  // what n counted occurrences and the bias add to token v; -0, which changes no value, is nothing
   auto summand = [&](int n, int v) {
-    float x = n > 0 ? -(f * (float)n) - pr : 0.0f;
+    float x = n > 0 ? -(f * (float)n) - pr : -0.0f;
     if constexpr (kBias) x += bias[v];
     return x;
   };
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
       const uint32_t on = (c & kAdjPath) != 0;
       paths |= on << i;
       seen |= (uint32_t)(rep && (c & kAdjSeen)) << i;
-      mine |= (uint32_t)(!on && (c != 0 || add[i] != 0.0f)) << i;
+      mine |= (uint32_t)(!on && ((rep && (c & kAdjSeen)) || add[i] != 0.0f)) << i;
     }
     for (int t = t0; t < t1; ++t) {
       uint32_t ok = kAll;
@@ -296,10 +296,11 @@ __global__ __launch_bounds__(kAdjBlock) void kr_adjust(const typename E::elem *l
     T_ e = src[at];
     const int n = (int)(c & kAdjCount) + m;
     const float add = summand(n, v), z = E::at(src, at);
-    float y = rep && (m > 0 || (c & kAdjSeen)) ? scaled(z, add) : z + add;
+    const bool times = rep && (m > 0 || (c & kAdjSeen));
+    float y = times ? scaled(z, add) : z + add;
     if (!ok) y = kNegInf;
     if (poison) y = nan;
-    if (m > 0 || (c & ~kAdjPath) != 0 || add != 0.0f || !ok || poison) {
+    if (times || add != 0.0f || !ok || poison) {
       if constexpr (sizeof(T_) == 4) e = y;
       else e = (T_)pack_bf16(y, y);
     }
