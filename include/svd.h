@@ -370,7 +370,10 @@ int svd_select_and_verify_noalloc(const void *p_logits, const void *q_logits,
  * i % 32 of anc[b][t][i / 32] says that node i is on node t's path, t itself
  * and the root included.  The verifier's row of node t predicts the token
  * after t, so the row pool [B * T][V] is what svd_select_and_verify_rows reads.
- * Limits: 1 <= T <= SVD_MAX_NODES, B * T < 2^30.
+ * Limits: 1 <= T <= SVD_MAX_NODES, B * T < 2^30.  A call must also fit one launch,
+ * below 2^32 threads (SVD_EINVAL otherwise): svd_draft_tree takes 1024 per prefix; the
+ * cache calls head_dim / 8 per token, head and array; the others up to 512 per
+ * prefix and group of rows, times the kv heads and parts, or ranges of the vocabulary.
  */
 #define SVD_MAX_NODES 4096
 

@@ -5,7 +5,10 @@
 
 namespace {
 
-constexpr int64_t kGridMax = ((int64_t)1 << 31) - 1;
+// A launch holds fewer than 2^32 threads.
+bool grid_ok(int64_t blocks, int64_t threads) {
+  return blocks >= 1 && blocks <= (((int64_t)1 << 32) - 1) / threads;
+}
 
 bool tree_sizes_ok(int64_t B, int32_t T) {
   return B >= 1 && T >= 1 && T <= SVD_MAX_NODES && B < ((int64_t)1 << 30) / T;
@@ -46,7 +49,7 @@ int write_rows(const void *k, const void *v, int64_t ks, int64_t vs, const int32
   using T_ = typename E::elem;
   constexpr int kRows = kCacheBlock / (D / 8);
   const int64_t per_b = (T * c.Hkv * 2 + kRows - 1) / kRows;
-  if (B > kGridMax / per_b) return SVD_EINVAL;
+  if (B > ((int64_t)1 << 32) / per_b || !grid_ok(B * per_b, kCacheBlock)) return SVD_EINVAL;
   CallTimer tm;
   SVD_LAUNCH(tm, SVD_KERNEL_CACHE_WRITE, s, kr_cache_write<E, kVec, kE4M3, D>,
              dim3((unsigned)(B * per_b)), dim3(kCacheBlock), s, static_cast<const T_ *>(k),
@@ -71,7 +74,7 @@ int read_rows(const CacheView &c, const int32_t *start, const int32_t *count, in
   using T_ = typename E::elem;
   constexpr int kRows = kCacheBlock / (D / 8);
   const int64_t per_b = (N * c.Hkv * 2 + kRows - 1) / kRows;
-  if (B > kGridMax / per_b) return SVD_EINVAL;
+  if (B > ((int64_t)1 << 32) / per_b || !grid_ok(B * per_b, kCacheBlock)) return SVD_EINVAL;
   CallTimer tm;
   SVD_LAUNCH(tm, SVD_KERNEL_CACHE_READ, s, kr_cache_read<E, kE4M3, D>, dim3((unsigned)(B * per_b)),
              dim3(kCacheBlock), s, c, start, count, N, per_b, static_cast<T_ *>(k),
@@ -134,8 +137,9 @@ bool attn_sizes_ok(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int
   if (D != 64 && D != 128) return false;
   if (room < 1 || room >= (int64_t)1 << 31) return false;
   const AttnPlan p = attn_plan(B, T, Hq, Hkv, D, room);
-  const int64_t units = B * Hkv * p.S;
-  return units < kGridMax / p.m_tiles - 8;
+  const int64_t threads = 64 * p.wq * p.wt + (p.nt == 1 ? kAttnLoaders : 0);
+  return B <= ((int64_t)1 << 32) / Hkv &&
+         grid_ok(((B * Hkv * p.S + 7) / 8 * 8) * p.m_tiles, threads);
 }
 
 size_t attn_ms_offset(int64_t rows, int S, int D) {
@@ -196,7 +200,7 @@ int svd_draft_tree(const int32_t *drafts, const int32_t *root, int64_t B, int32_
                    int32_t *n_nodes, int32_t *p_index, void *hip_stream) {
   if (!drafts || !tokens || !parent || !depth || !anc || !n_nodes || !p_index) return SVD_EINVAL;
   if (K < 1 || K > SVD_MAX_K || gamma < 1 || gamma > SVD_MAX_GAMMA || !tree_sizes_ok(B, T) ||
-      B >= ((int64_t)1 << 31) / ((int64_t)K * (gamma + 1)))
+      B >= ((int64_t)1 << 31) / ((int64_t)K * (gamma + 1)) || !grid_ok(B, kTreeBlock))
     return SVD_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   CallTimer tm;
@@ -360,7 +364,7 @@ int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
   a.n_ranges = (int)nr;
   a.n_chunks = (T + a.row_step - 1) / a.row_step;
   const int64_t blocks = B * nr * a.n_chunks;
-  if (blocks > kGridMax) return SVD_EINVAL;
+  if (!grid_ok(blocks, kAdjBlock)) return SVD_EINVAL;
   const bool vec = ((size_t)V * es) % 16 == 0 && ((uintptr_t)logits) % 16 == 0 &&
                    ((uintptr_t)out) % 16 == 0;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
