@@ -459,6 +459,7 @@ int svd_cache_read(const svd_cache_t *cache, const int32_t *start, const int32_t
  *   q      bf16 rows [q_heads][head_dim]; token (b, t) starts at element
  *          (b * T + t) * q_stride (a multiple of 8; q 16-byte aligned)
  *   out    [B][T][q_heads][head_dim] bf16 (16-byte aligned);  lse [B][T][q_heads] fp32, nullable
+ *          out must not overlap the memory from q's first to its last element
  * The running maximum, the sums and the accumulation are fp32; probabilities are
  * rounded to bf16 as an operand of the second product.  A row that attends to
  * nothing gives 0 and lse = -inf.  What a row does not attend to does not reach

@@ -284,6 +284,13 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
     return SVD_EINVAL;
   if (workspace_bytes < svd_tree_attention_workspace_bytes(B, T, q_heads, c.Hkv, D, room))
     return SVD_EWORKSPACE;
+  // a row with values that are not finite reads its query again while pieces of its
+  // output are written already
+  const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+  const uint64_t row = (uint64_t)q_heads * D * 2;
+  if (q0 < o0 + (uint64_t)(B * T) * row &&
+      o0 < q0 + (uint64_t)(B * T - 1) * ((uint64_t)q_stride * 2) + row)
+    return SVD_EINVAL;
   const AttnPlan p = attn_plan(B, T, q_heads, c.Hkv, D, room);
   AttnArgs a;
   a.q = static_cast<const uint16_t *>(q);

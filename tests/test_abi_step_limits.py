@@ -43,3 +43,10 @@ def test_more_threads_than_a_launch_holds(svd):  # noqa: F811
     assert attend(svd, cache(svd), B=most // 2 + 1, T=1, Hq=2) == svd.SVD_EINVAL
     assert attend(svd, cache(svd), B=most // 2, T=1, Hq=2) == svd.SVD_EWORKSPACE
     assert adjust(svd, 1 << 24, 100) == svd.SVD_EINVAL            # 256 a prefix and range
+
+
+@pytest.mark.parametrize("out", [1 << 16, (1 << 16) + 512, (1 << 16) - 2560, (1 << 16) + 5 * 768 + 256])
+def test_attention_does_not_write_over_its_queries(svd, out):  # noqa: F811
+    # 6 tokens of 4 heads of 64, 384 elements apart: q from 65536 to 65536 + 5 * 768 + 512
+    kw = dict(q=1 << 16, qs=384, ws=1 << 20, n=1 << 20)
+    assert attend(svd, cache(svd), out=out, **kw) == svd.SVD_EINVAL
