@@ -403,10 +403,13 @@ int svd_draft_tree(const int32_t *drafts, const int32_t *root, int64_t B, int32_
  * SVD_CACHE_E4M3 holds 8-bit codes (OCP E4M3) with one power of two per (token,
  * head) row, the smallest 2^e with max |x| <= 448 * 2^e over the row's finite
  * values, e in [-126, 120]: k_scale and v_scale [n_pages][kv_heads][page] hold
- * e + 127 (a byte from 1 to 254).  A value is code * 2^e, exactly, in bf16 too (what
- * would round to 2^128 is held as 240 * 2^120); an infinity or NaN is held as NaN.  Limits: head_dim 64 or 128; page a power of
- * two from 16 to 1024; max_pages * page < 2^31; k and v 16-byte aligned, k_scale
- * and v_scale 4-byte aligned.  The struct is read during the call only.
+ * e + 127 (a byte from 1 to 247).  A value is code * 2^e, exactly (what would round
+ * to 2^128 is held as 240 * 2^120); an infinity or NaN is held as NaN.  It is exact in
+ * bf16 too where e >= -124; at e = -126 and -125, codes can have bits below 2^-133, bf16's
+ * least step, and are rounded to it (nearest even) wherever a value becomes bf16, in a
+ * read as in the attention.  Limits: head_dim 64 or 128; page a power of two from 16
+ * to 1024; max_pages * page < 2^31; k and v 16-byte aligned, k_scale and v_scale
+ * 4-byte aligned.  The struct is read during the call only.
  */
 typedef enum {
   SVD_CACHE_BF16 = 0,

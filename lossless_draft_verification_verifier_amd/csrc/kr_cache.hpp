@@ -6,8 +6,9 @@
 // as 8-bit codes and one power of two, the smallest 2^e with
 // max |x| <= 448 * 2^e, as the byte e + 127.  A power of two costs none of
 // the codes' relative precision (they are floating), makes x * 2^-e exact, so
-// the one rounding is the code's own, and makes code * 2^e exact in bf16: a
-// reader loses nothing by widening to bf16.
+// the one rounding is the code's own, and makes code * 2^e exact in bf16 for
+// e >= -124: a reader loses nothing by widening to bf16.  (At e = -126 and -125
+// the lowest codes end below 2^-133, the least step of bf16.)
 //
 // Both kernels are bound by HBM: a row is read once and written once, D / 8 lanes
 // per row with 16-byte accesses on the wide side.  32768 tokens of 8 heads of 128,
