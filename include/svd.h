@@ -391,7 +391,8 @@ int svd_select_and_verify_noalloc(const void *p_logits, const void *q_logits,
  *           position: b * T + node of the position before it; -1 past a draft's end
  * Unused nodes: token -1, parent -1, depth 0, no bits.  T = 1 + K * gamma always
  * suffices; a prefix with more nodes than T is a data error: n_nodes = -1, its
- * p_index -1 (so that svd_select_and_verify_rows gives it -1 outputs).
+ * p_index -1 (so that svd_select_and_verify_rows gives it -1 outputs).  That call takes
+ * whole drafts only: it gives -1 outputs as well to a prefix with a draft that ends early.
  */
 int svd_draft_tree(const int32_t *drafts, const int32_t *root, int64_t B, int32_t K, int32_t gamma,
                    int32_t T, int32_t *tokens, int32_t *parent, int32_t *depth, uint32_t *anc,
@@ -486,7 +487,10 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
  * verification call (V = the verifier's vocabulary; T = 1: plain decoding).  Row
  * (b, t) predicts the token after node t; its tokens are the history of prefix b
  * and the nodes on its path (tokens[b][i] for the bits of anc[b][t]; anc NULL: nodes
- * 0..t; tokens NULL: none).  Ids outside [0, V) are ignored.  In this order, as one
+ * 0..t; tokens NULL: none).  Ids outside [0, V) are ignored.  The root is on every
+ * path and counts as generated, so the history leaves the last committed token out;
+ * where that is the prompt's last token, it goes into the history, as prompt, and the
+ * root's token is -1.  In this order, as one
  * factor (z > 0: the rounded 1 / repetition) and one summand in fp32, then rounded to
  * the logits' type:
  *   z > 0 ? z / repetition[b] : z * repetition[b]   for a token that occurs;

@@ -818,7 +818,8 @@ def draft_tree(drafts, root=None, n_max=None, stream=None):
     committed tokens, n_max room for nodes (default 1 + K * gamma, which always
     suffices).  Returns tokens, parent, depth [B,n_max], anc [B,n_max,W] (bit i % 32
     of word i // 32: node i is on the node's path), n_nodes [B] and p_index
-    [B,K,gamma+1], the rows of the pool [B * n_max, V] for select_and_verify_rows."""
+    [B,K,gamma+1], the rows of the pool [B * n_max, V] for select_and_verify_rows (which
+    takes whole drafts: one that ends early, at a negative token, gives its prefix -1)."""
     if stream is not None:
         return _on(stream, drafts, draft_tree, drafts, root, n_max)
     torch = _torch()
@@ -1007,7 +1008,7 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
     """Penalties, biases and grammar masks on logits [B,T,V] (bf16 or fp32), row
     (b, t) after node t of a tree.  history [B,H] int32 with hist_len [B] tokens
     used (prompt_len [B] of them the prompt), tokens [B,T] and anc [B,T,W] of the
-    tree; repetition, frequency, presence [B] fp32; bias = (offsets [B+1] int32,
+    tree (the root counts as generated: the history does not hold it, too); repetition, frequency, presence [B] fp32; bias = (offsets [B+1] int32,
     tokens int32, values fp32); allow [n,ceil(V/32)] int32 bit masks and
     allow_index [B,T] int32 (negative: none).  out: default a new tensor; logits
     itself for a change in place.  Returns out."""
