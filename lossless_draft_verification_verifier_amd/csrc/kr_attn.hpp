@@ -16,24 +16,33 @@
 // (by the conversion instruction; exact down to 2^-124), and V transposed.  WQ waves split the rows,
 // and where these are few, WT waves split the tile's tokens and merge at the end.  One
 // barrier per tile.  LDS rows hold 16-byte blocks at an index xor'ed with the row,
-// so that 16 lanes reading 16 rows touch all banks.
+// so that 16 lanes reading 16 rows touch all banks.  The 8-byte stores of V^T do not:
+// lanes of different elements meet in a block, and of all LDS cycles 39 % (the 9-node
+// batch below) and 31 % (the trees) are bank conflicts.
 //   - Up to 64 rows (NT = 1) the cache's bytes are what counts: 4 waves of their own
 //     keep the next PF tiles on their way in registers and write one to LDS while
 //     the others compute the one before, two workgroups per CU.  Against one kind of wave
 //     with the next tile in registers, 256 requests of 9 nodes over 1 to 4096 E4M3
-//     tokens: 360 -> 287 us.
+//     tokens: 360 -> 293 us.
 //   - With more rows (NT = 2) the products are: all 8 waves compute, 32 rows each, and
 //     bring keys or values, the two waves of a SIMD at opposite ends of a step.
-// p is rounded to bf16 once, as the operand of the second product: an operand of the
-// matrix instruction has no more bits beside bf16 values.  m, l and O stay in 32
-// bits and l sums the unrounded p.
+// p is rounded to bf16 once, as the operand of the second product, by at most 2^-8 of
+// itself; m, l and O stay in 32 bits and l sums the unrounded p.  The rounding is a
+// choice: with the rest of p as a second bf16 operand the outputs' error is their own
+// rounding alone, root mean square 4.0e-4 instead of 5.3e-4 (9-node batch below, outputs
+// of 0.24; 1.3e-5 instead of 1.9e-5 for the trees, of 0.008), but the second product
+// and the packing double: 297 -> 325 us, 363 -> 456 for the trees, 56 -> 62 for 24
+// requests of 33 nodes.  An output is rounded to bf16 in any case, and the errors of many
+// tokens' p average out, so one operand is kept.
 //
-// Bounds, on one MI355X.  The 9-node batch above: 1.12 GB in 287 us, 3.9 TB/s; the
-// tiles alone, nothing computed, take 246 us, and a copy of as many bytes 230.  Trees of
-// 65 to 129 nodes over 30000 bf16 tokens, 4 requests: 200 GFLOP in 367 us, 544
-// TFLOP/s; the matrix units are busy for a quarter of that and the vector units for a
-// third, and what is left is waiting inside a tile: a wave's scores, maxima,
-// exponentials and second product depend on each other, and two waves per SIMD are all
+// Bounds, on one MI355X.  The 9-node batch above: 1.12 GB in 293 us, 3.8 TB/s; the
+// tiles alone, nothing computed, take 246 us, a copy of as many bytes 230, and at the
+// rate of a plain read (6.9 TB/s) they would take 163.  Trees of 65 to 129 nodes over
+// 30000 bf16 tokens, 4 requests: 200 GFLOP in 363 us, 550 TFLOP/s; the matrix units are
+// busy for a quarter of that and the vector units for a third.  Two things are left.
+// Rows are dealt to workgroups by T, not by a prefix's own nodes: these prefixes have
+// rows for 51 of the 80 waves they hold.  And inside a tile a wave's scores, maxima,
+// exponentials and second product depend on each other, with two waves per SIMD all
 // that the registers allow.
 //
 // The tiles of a prefix are split evenly over S workgroups when there are few

@@ -12,9 +12,9 @@
 //
 // Both kernels are bound by HBM: a row is read once and written once, D / 8 lanes
 // per row with 16-byte accesses on the wide side.  32768 tokens of 8 heads of 128,
-// bf16 to E4M3 and back: 61 us to write (3.3 TB/s: a row waits for its length, then its
-// page; four rows per lane group took 57 but cost a single token 1.4 us) and 40 us to
-// read (5.0 TB/s).
+// bf16 to E4M3 and back: 57 us to write (3.5 TB/s: a row waits for its length, then its
+// page, then its source, which is loaded for a row with a page only; four rows per lane
+// group saved 4 us but cost a single token 1.4) and 37 us to read (5.5 TB/s).
 #pragma once
 
 #include "svd_device.hpp"

@@ -10,9 +10,12 @@
 // bits: no walk over single nodes.
 //
 // Bound by latency: a call reads K*G tokens per prefix and its steps depend on
-// each other, so one workgroup does a whole prefix with five barriers.  8 drafts of
-// 16 tokens: 4.5 us; 64 prefixes with 16 drafts of 32: 15.8 us (20.8 with 512 threads
-// and a search for every word's owner instead of a table).
+// each other, so one workgroup does a whole prefix.  8 drafts of 16 tokens: 4.6 us;
+// 64 prefixes with 16 drafts of 32: 15.6 us (20.8 with 512 threads and a search for
+// every word's owner instead of a table).  There the ancestor words are the largest
+// part: 513 nodes of 17 words on 32 lanes each, and every word walks the chain of par by
+// itself, one dependent read of LDS after another; without the walk a call takes less
+// than the 11 us that its host side does.
 #pragma once
 
 #include "svd_device.hpp"
