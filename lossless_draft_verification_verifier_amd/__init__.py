@@ -16,6 +16,8 @@ Tensor conveniences that allocate the outputs and the workspace with torch:
     verify, select_and_verify, greedy_verify, greedy_select_and_verify,
     select_and_verify_rows, verify_window, cps_lattice, cps_beam, adl_next, workspace_bytes;
     draft_tree, kv_cache, cache_write, cache_read, tree_attention, adjust_logits
+  Their stream argument is the handle of the stream to run on (an int; default the
+  current one); what a call allocates, its results too, belongs to that stream.
 Kernel timing: timing_library() loads ``libsvd_timed.so`` (the same kernels with
 HIP-event timing compiled in, ``include/svd_timing.h``) as a Library whose raw
 entry points are those above plus svd_profile_enable and svd_profile_read.
@@ -1008,10 +1010,11 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
     """Penalties, biases and grammar masks on logits [B,T,V] (bf16 or fp32), row
     (b, t) after node t of a tree.  history [B,H] int32 with hist_len [B] tokens
     used (prompt_len [B] of them the prompt), tokens [B,T] and anc [B,T,W] of the
-    tree (the root counts as generated: the history does not hold it, too); repetition, frequency, presence [B] fp32; bias = (offsets [B+1] int32,
-    tokens int32, values fp32); allow [n,ceil(V/32)] int32 bit masks and
-    allow_index [B,T] int32 (negative: none).  out: default a new tensor; logits
-    itself for a change in place.  Returns out."""
+    tree (the root counts as generated: the history does not hold it, too);
+    repetition, frequency, presence [B] fp32; bias = (offsets [B+1] int32, tokens
+    int32, values fp32); allow [n,ceil(V/32)] int32 bit masks and allow_index [B,T]
+    int32 (negative: none).  out: default a new tensor; logits itself for a change in
+    place.  Returns out."""
     if stream is not None:
         return _on(stream, logits, adjust_logits, logits, history, hist_len, prompt_len, tokens,
                    anc, n_rows, repetition, frequency, presence, bias, allow, allow_index, out)

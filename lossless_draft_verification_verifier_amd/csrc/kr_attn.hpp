@@ -12,10 +12,10 @@
 // operand the second one wants there, so p never crosses lanes.
 //
 // A workgroup takes up to 16 * NT * WQ rows and walks tiles of TK tokens, written to
-// LDS once for all rows: widened from E4M3 to bf16 with the row's power of two
-// (by the conversion instruction; exact down to 2^-124), and V transposed.  WQ waves split the rows,
-// and where these are few, WT waves split the tile's tokens and merge at the end.  One
-// barrier per tile.  LDS rows hold 16-byte blocks at an index xor'ed with the row,
+// LDS once for all rows: widened from E4M3 to bf16 with the row's power of two (by the
+// conversion instruction; exact down to 2^-124), and V transposed.  WQ waves split the
+// rows, and where these are few, WT waves split the tile's tokens and merge at the end.
+// One barrier per tile.  LDS rows hold 16-byte blocks at an index xor'ed with the row,
 // so that 16 lanes reading 16 rows touch all banks.  The 8-byte stores of V^T do not:
 // lanes of different elements meet in a block, and of all LDS cycles 39 % (the 9-node
 // batch below) and 31 % (the trees) are bank conflicts.
