@@ -411,7 +411,7 @@ def _plain_pages(s):
     upto, gone = grow.cumsum(0), shrink.cumsum(0)
     ok = (grow == 0) | (upto <= count)
     now = torch.where(ok, need, held)
-    taken = torch.where(ok, upto, 0).amax()
+    taken = torch.where(ok & (grow > 0), upto, 0).amax()
     at, was, new = j.unsqueeze(0), held.unsqueeze(1), now.unsqueeze(1)
     # granted pages come from the head of the ring in sequence order
     from_ring = ring.long()[(head + (upto - grow).unsqueeze(1) + at - was) % n]
