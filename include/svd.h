@@ -520,6 +520,128 @@ int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
                       const uint32_t *allow, const int32_t *allow_index, int32_t n_masks,
                       void *hip_stream);
 
+/*
+ * Filtered logits: the tokens of a row of logits [B][T][V] that its prefix's settings
+ * keep, before a verification call (which is lossless for the filtered laws then) or a
+ * draw.  With w = exp((z - max z) / temperature[b]) kept are, in this order,
+ *   the tokens with w >= min_p[b] (0 or less: all; the largest logit always);
+ *   of those the first top_k[b] by falling logit, the lower index first among equal
+ *     ones (0 or less, or at least V: all);
+ *   of those the shortest beginning of that order whose weight is at least top_p[b] of
+ *     the weight of all of them (1 or more: all; at least one token).
+ * Each of temperature (1), top_k, top_p, min_p [B] is nullable.  A temperature of 0
+ * keeps the first token with the largest logit alone.  Weights are held as whole
+ * multiples of 2^-s, s = 62 - ceil(log2 V), 50 at most, of the largest one, rounded once
+ * from fp64, and their sums are exact: results depend neither on how the work is
+ * divided nor on any order.
+ *
+ * svd_filter_logits: out [B][T][V] holds the logits as they are, not divided by the
+ * temperature, and -inf for every token that is not kept.  out may be logits itself, but
+ * must not overlap it otherwise.
+ *
+ * svd_sample: K tokens per row, for K drafts of one set of marginals.  token [B][K][T]
+ * out: the first token by index up to which the kept weights exceed u times their sum;
+ * logprob [B][K][T] out, nullable, fp32: the logarithm of the token's share of it.
+ *   uniforms [B][K][T] fp64, u in [0, 1); NULL: u = U(seed, row_base + b, k * T + t, 4)
+ *
+ * Rows from n_rows[b] on (nullable: T) are left as they were.  Data errors: a row with a
+ * NaN or +inf, or all -inf, and every row of a prefix whose temperature is negative, not
+ * finite or NaN, whose top_p or min_p is NaN or whose n_rows is out of range, become NaN rows
+ * (a verification call reports them as -1), or token -1 and logprob NaN; a u outside [0, 1)
+ * gives its own draw token -1.  Limits: those of the tree calls; 1 <= K <= SVD_MAX_K,
+ * B * T * K < 2^31, B * T < 2^22.  No workspace.
+ */
+int svd_filter_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t B, int32_t T,
+                      int32_t V, const int32_t *n_rows, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p,
+                      void *hip_stream);
+int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int32_t V, int32_t K,
+               const int32_t *n_rows, const float *temperature, const int32_t *top_k,
+               const float *top_p, const float *min_p, const double *uniforms, uint64_t seed,
+               uint64_t row_base, int32_t *token, float *logprob, void *hip_stream);
+
+/*
+ * svd_tree_attention for batches that share prefixes, and for shaped scores.
+ *
+ * Groups: sequences share_off[g] .. share_off[g+1] - 1 (share_off [n_groups+1],
+ * nondecreasing, from 0 to B at most; NULL with n_groups = 0) are a group.  The tokens of
+ * the pages that the block tables of all of its sequences begin with are read and
+ * multiplied once for the group.  What is computed does not depend on the grouping, but
+ * for roundings; sequences outside every group, groups that have no page in common and
+ * offsets out of order share nothing.
+ * Scores: z = scale * q . k becomes cap * tanh(z / cap) when cap > 0, and then loses
+ * slopes[h] * distance when slopes [q_heads] is not NULL, the distance being the row's
+ * position less the token's; node t is at position ctx_len[b] + depth[b][t] (depth
+ * [B][T], needed with slopes and anc; without anc, for a chain, it is not read).
+ * Everything else is as for svd_tree_attention, whose results a call without groups, cap and
+ * slopes gives bit for bit.  cap must be finite and not negative.  Workspace:
+ * svd_prefix_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_pages *
+ * page, n_groups) bytes (0 for sizes out of range: also n_groups > B, or, with groups,
+ * B * T * q_heads / kv_heads of 2^31 or more), 256-byte aligned.
+ */
+size_t svd_prefix_attention_workspace_bytes(int64_t B, int32_t T, int32_t q_heads,
+                                            int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                                            int64_t n_groups);
+int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stride,
+                         const int32_t *ctx_len, const int32_t *n_nodes, const uint32_t *anc,
+                         const int32_t *depth, const int32_t *share_off, int64_t n_groups,
+                         float scale, float cap, const float *slopes, int64_t B, int32_t T,
+                         int32_t q_heads, void *out, float *lse, void *workspace,
+                         size_t workspace_bytes, void *hip_stream);
+
+/*
+ * Block tables from lengths, without a trip to the host.  Free pages are a ring:
+ * free_ring [n_pages] holds state[1] page indices from place state[0] on, modulo n_pages.
+ * Sequence b shall have pages for length[b] tokens: max(shared[b], ceil(length[b] /
+ * page)) entries of its row of block_table, where held[b] are in use.  The first
+ * shared[b] (nullable: 0) are another's, such as a common prefix's: they are never given back.
+ *   A sequence that needs more takes them from the ring's head, in sequence order; if
+ *   the sequences up to and with b need more than the ring holds, b gets none and
+ *   nothing of it changes.
+ *   One that needs fewer gives its last ones back, behind the ring's end, in sequence
+ *   order; its entries become -1.  Pages given back are there for later calls, not this one.
+ *   state_out [2], held_out [B], table_out [B][max_pages] out: each its input itself (a
+ *   change in place; table entries that do not change are not touched) or apart from it
+ *   (then all of the table is written)
+ *   room [B] out: the tokens that b has pages for, -1 for a length, held or shared out of
+ *   range (nothing of such a sequence changes), or for all of them, and nothing changes, when
+ *   the state is out of range or the ring would hold more than n_pages
+ * page as in svd_cache_t; B * max_pages < 2^31.  Workspace:
+ * svd_cache_pages_workspace_bytes(B) bytes, 256-byte aligned.
+ */
+size_t svd_cache_pages_workspace_bytes(int64_t B);
+int svd_cache_pages(const int32_t *length, const int32_t *shared, int64_t B, int32_t max_pages,
+                    int32_t page, int64_t n_pages, int32_t *free_ring, const int32_t *state,
+                    const int32_t *held, const int32_t *block_table, int32_t *state_out,
+                    int32_t *held_out, int32_t *table_out, int32_t *room, void *workspace,
+                    size_t workspace_bytes, void *hip_stream);
+
+/*
+ * Slots of packed tokens: sequence b brings n_new[b] tokens, to the positions from
+ * ctx_len[b] on, and the sequences' tokens lie one after another in N places.
+ *   row_off [B+1] out  the place of each sequence's first token, then their number (at
+ *                      most 2^31 - 1; may pass N: such tokens have no place)
+ *   seq, pos [N] out   a token's sequence and position;  slot [N] int64 out  its page *
+ *                      (tokens a page) + its place there, -1 where the position has no
+ *                      page.  All three are -1 behind the last token.
+ * A sequence whose ctx_len or n_new is negative, or whose positions pass 2^31 - 1, brings
+ * none.  No workspace.
+ */
+int svd_cache_slots(const int32_t *ctx_len, const int32_t *n_new, const int32_t *block_table,
+                    int64_t B, int32_t max_pages, int32_t page, int64_t n_pages, int64_t N,
+                    int32_t *row_off, int32_t *seq, int32_t *pos, int64_t *slot,
+                    void *hip_stream);
+
+/*
+ * Write N packed tokens to the cache, token i to slot[i] (a slot outside the pages is
+ * skipped); k, v rows [kv_heads][head_dim] of dtype, token i at element i * k_stride
+ * (v_stride).  The cache's block_table and max_pages are not read.  Two tokens of one call with
+ * one slot leave it with unspecified contents.
+ */
+int svd_cache_write_slots(const svd_cache_t *cache, const void *k, const void *v,
+                          svd_dtype_t dtype, int64_t k_stride, int64_t v_stride,
+                          const int64_t *slot, int64_t N, void *hip_stream);
+
 /* Static text for a status code. */
 const char *svd_strerror(int status);
 

@@ -52,7 +52,12 @@ enum {
   SVD_KERNEL_TREE_ATTENTION = 19, /* attention of the tree over the cache                 */
   SVD_KERNEL_ATTENTION_JOIN = 20, /* merge of the parts of a split attention              */
   SVD_KERNEL_ADJUST = 21,       /* penalties, biases and masks on logit rows              */
-  SVD_KERNEL_COUNT = 22
+  SVD_KERNEL_PAGES = 22,        /* block tables from lengths: the plan, the pages' moves  */
+  SVD_KERNEL_SLOTS = 23,        /* packed tokens' sequences, positions and slots          */
+  SVD_KERNEL_FILTER = 24,       /* tokens that temperature, min-p, top-k and top-p keep   */
+  SVD_KERNEL_SAMPLE = 25,       /* draws among the kept tokens                            */
+  SVD_KERNEL_SHARE = 26,        /* tokens that the sequences of a group have in common    */
+  SVD_KERNEL_COUNT = 27
 };
 
 int svd_profile_enable(unsigned kernel_mask);

@@ -11,11 +11,15 @@ arguments take an int address or a tensor):
     svd_verify_window, svd_cps_workspace_bytes, svd_cps_lattice, svd_cps_beam,
     svd_adl_next, svd_select_and_verify_noalloc, svd_strerror; around the verification step:
     svd_draft_tree, svd_cache_write, svd_cache_read, svd_tree_attention_workspace_bytes,
-    svd_tree_attention, svd_adjust_logits
+    svd_tree_attention, svd_adjust_logits, svd_cache_pages_workspace_bytes, svd_cache_pages,
+    svd_cache_slots, svd_cache_write_slots, svd_filter_logits, svd_sample,
+    svd_prefix_attention_workspace_bytes, svd_prefix_attention
 Tensor conveniences that allocate the outputs and the workspace with torch:
     verify, select_and_verify, greedy_verify, greedy_select_and_verify,
     select_and_verify_rows, verify_window, cps_lattice, cps_beam, adl_next, workspace_bytes;
-    draft_tree, kv_cache, cache_write, cache_read, tree_attention, adjust_logits
+    draft_tree, kv_cache, cache_write, cache_read, tree_attention, adjust_logits;
+    page_pool, cache_pages, cache_slots, cache_write_slots, filter_logits, sample,
+    prefix_attention
   Their stream argument is the handle of the stream to run on (an int; default the
   current one); what a call allocates, its results too, belongs to that stream.
 Kernel timing: timing_library() loads ``libsvd_timed.so`` (the same kernels with
@@ -44,7 +48,7 @@ SVD_CACHE_BF16, SVD_CACHE_E4M3 = 0, 1
 KERNELS = ("rowstats", "select", "draw_pass", "draw_pick", "beta", "mark", "pool_stats",
            "alpha_rows", "lattice", "beam", "lattice_len", "combine", "rowstats_split",
            "rowstats_live", "adl", "beta_combine", "draft_tree", "cache_write", "cache_read",
-           "tree_attention", "attention_join", "adjust")
+           "tree_attention", "attention_join", "adjust", "pages", "slots", "filter", "sample", "share")
 SVD_RULE_STANDARD, SVD_RULE_GREEDY = 0, 1
 
 C_EXPORTS = ("svd_workspace_bytes", "svd_verify", "svd_select_and_verify", "svd_greedy_verify",
@@ -53,7 +57,9 @@ C_EXPORTS = ("svd_workspace_bytes", "svd_verify", "svd_select_and_verify", "svd_
              "svd_cps_lattice", "svd_cps_beam", "svd_adl_next", "svd_select_and_verify_noalloc",
              "svd_draft_tree", "svd_cache_write", "svd_cache_read",
              "svd_tree_attention_workspace_bytes", "svd_tree_attention", "svd_adjust_logits",
-             "svd_strerror")
+             "svd_cache_pages_workspace_bytes", "svd_cache_pages", "svd_cache_slots",
+             "svd_cache_write_slots", "svd_filter_logits", "svd_sample",
+             "svd_prefix_attention_workspace_bytes", "svd_prefix_attention", "svd_strerror")
 TIMING_EXPORTS = ("svd_profile_enable", "svd_profile_read")
 
 _M64 = 0xFFFFFFFFFFFFFFFF
@@ -128,6 +134,25 @@ def _declare(L: ctypes.CDLL, timing: bool) -> ctypes.CDLL:
     L.svd_adjust_logits.restype = ctypes.c_int
     L.svd_adjust_logits.argtypes = [vp, vp, ctypes.c_int, i64, i32, i32, vp, vp, i64, vp, vp, vp,
                                     vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, i32, vp]
+    L.svd_cache_pages_workspace_bytes.restype = sz
+    L.svd_cache_pages_workspace_bytes.argtypes = [i64]
+    L.svd_cache_pages.restype = ctypes.c_int
+    L.svd_cache_pages.argtypes = [vp, vp, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                  sz, vp]
+    L.svd_cache_slots.restype = ctypes.c_int
+    L.svd_cache_slots.argtypes = [vp, vp, vp, i64, i32, i32, i64, i64, vp, vp, vp, vp, vp]
+    L.svd_cache_write_slots.restype = ctypes.c_int
+    L.svd_cache_write_slots.argtypes = [vp, vp, vp, ctypes.c_int, i64, i64, vp, i64, vp]
+    L.svd_filter_logits.restype = ctypes.c_int
+    L.svd_filter_logits.argtypes = [vp, vp, ctypes.c_int, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.svd_sample.restype = ctypes.c_int
+    L.svd_sample.argtypes = [vp, ctypes.c_int, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, u64, u64,
+                             vp, vp, vp]
+    L.svd_prefix_attention_workspace_bytes.restype = sz
+    L.svd_prefix_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i64, i64]
+    L.svd_prefix_attention.restype = ctypes.c_int
+    L.svd_prefix_attention.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, i64, f32, f32, vp, i64, i32,
+                                       i32, vp, vp, vp, sz, vp]
     L.svd_strerror.restype = ctypes.c_char_p
     L.svd_strerror.argtypes = [ctypes.c_int]
     if timing:
@@ -304,6 +329,59 @@ class Library:
             _addr(bias_tok), _addr(bias_val), int(n_bias), _addr(allow), _addr(allow_index),
             int(n_masks), _addr(hip_stream)))
 
+    def svd_cache_pages_workspace_bytes(self, B: int) -> int:
+        return int(self._lib.svd_cache_pages_workspace_bytes(B))
+
+    def svd_cache_pages(self, length, shared, B, max_pages, page, n_pages, free_ring, state, held,
+                        block_table, state_out, held_out, table_out, room, workspace,
+                        workspace_bytes, hip_stream) -> int:
+        return int(self._lib.svd_cache_pages(
+            _addr(length), _addr(shared), int(B), int(max_pages), int(page), int(n_pages),
+            _addr(free_ring), _addr(state), _addr(held), _addr(block_table), _addr(state_out),
+            _addr(held_out), _addr(table_out), _addr(room), _addr(workspace),
+            int(workspace_bytes), _addr(hip_stream)))
+
+    def svd_cache_slots(self, ctx_len, n_new, block_table, B, max_pages, page, n_pages, N, row_off,
+                        seq, pos, slot, hip_stream) -> int:
+        return int(self._lib.svd_cache_slots(
+            _addr(ctx_len), _addr(n_new), _addr(block_table), int(B), int(max_pages), int(page),
+            int(n_pages), int(N), _addr(row_off), _addr(seq), _addr(pos), _addr(slot),
+            _addr(hip_stream)))
+
+    def svd_cache_write_slots(self, cache, k, v, dtype, k_stride, v_stride, slot, N,
+                              hip_stream) -> int:
+        return int(self._lib.svd_cache_write_slots(
+            _struct(cache), _addr(k), _addr(v), int(dtype), int(k_stride), int(v_stride),
+            _addr(slot), int(N), _addr(hip_stream)))
+
+    def svd_filter_logits(self, logits, out, dtype, B, T, V, n_rows, temperature, top_k, top_p,
+                          min_p, hip_stream) -> int:
+        return int(self._lib.svd_filter_logits(
+            _addr(logits), _addr(out), int(dtype), int(B), int(T), int(V), _addr(n_rows),
+            _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), _addr(hip_stream)))
+
+    def svd_sample(self, logits, dtype, B, T, V, K, n_rows, temperature, top_k, top_p, min_p,
+                   uniforms, seed, row_base, token, logprob, hip_stream) -> int:
+        return int(self._lib.svd_sample(
+            _addr(logits), int(dtype), int(B), int(T), int(V), int(K), _addr(n_rows),
+            _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), _addr(uniforms),
+            int(seed) & _M64, int(row_base) & _M64, _addr(token), _addr(logprob),
+            _addr(hip_stream)))
+
+    def svd_prefix_attention_workspace_bytes(self, B: int, T: int, q_heads: int, kv_heads: int,
+                                             head_dim: int, max_len: int, n_groups: int) -> int:
+        return int(self._lib.svd_prefix_attention_workspace_bytes(B, T, q_heads, kv_heads,
+                                                                  head_dim, max_len, n_groups))
+
+    def svd_prefix_attention(self, cache, q, q_stride, ctx_len, n_nodes, anc, depth, share_off,
+                             n_groups, scale, cap, slopes, B, T, q_heads, out, lse, workspace,
+                             workspace_bytes, hip_stream) -> int:
+        return int(self._lib.svd_prefix_attention(
+            _struct(cache), _addr(q), int(q_stride), _addr(ctx_len), _addr(n_nodes), _addr(anc),
+            _addr(depth), _addr(share_off), int(n_groups), float(scale), float(cap),
+            _addr(slopes), int(B), int(T), int(q_heads), _addr(out), _addr(lse), _addr(workspace),
+            int(workspace_bytes), _addr(hip_stream)))
+
     def svd_strerror(self, status: int) -> str:
         return self._lib.svd_strerror(int(status)).decode()
 
@@ -365,6 +443,14 @@ svd_cache_read = _default.svd_cache_read
 svd_tree_attention_workspace_bytes = _default.svd_tree_attention_workspace_bytes
 svd_tree_attention = _default.svd_tree_attention
 svd_adjust_logits = _default.svd_adjust_logits
+svd_cache_pages_workspace_bytes = _default.svd_cache_pages_workspace_bytes
+svd_cache_pages = _default.svd_cache_pages
+svd_cache_slots = _default.svd_cache_slots
+svd_cache_write_slots = _default.svd_cache_write_slots
+svd_filter_logits = _default.svd_filter_logits
+svd_sample = _default.svd_sample
+svd_prefix_attention_workspace_bytes = _default.svd_prefix_attention_workspace_bytes
+svd_prefix_attention = _default.svd_prefix_attention
 svd_strerror = _default.svd_strerror
 
 
@@ -879,10 +965,12 @@ def _cache_struct(cache, block_table, B):
         code, ks, vs = SVD_CACHE_BF16, None, None
     else:
         raise TypeError("a cache is torch.bfloat16 or torch.float8_e4m3fn, got %s" % dtype)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B,max_pages]")
     n_pages, heads, page, D = shape
-    mp = block_table.shape[1]
+    mp = 0
+    if block_table is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must be [B,max_pages]")
+        mp = block_table.shape[1]
     return CacheStruct(_ptr(k, "cache k", dev, dtype, shape), _ptr(v, "cache v", dev, dtype, shape),
                        ks, vs, _ptr(block_table, "block_table", dev, torch.int32, (B, mp)),
                        n_pages, mp, page, heads, D, code), dev
@@ -1057,3 +1145,239 @@ def adjust_logits(logits, history=None, hist_len=None, prompt_len=None, tokens=N
           _ptr(presence, "presence", dev, f32, b), off, tok, val, n_bias, allow,
           _ptr(allow_index, "allow_index", dev, i32, bt), n_masks)
     return out
+
+
+# --------------------------------------------------------------------------
+# A serving loop's other operators: block tables and slot maps of the cache,
+# filtered and sampled logits, attention over shared prefixes.
+
+def page_pool(n_pages, B, max_pages, device="cuda"):
+    """The block tables of B empty sequences and a ring of n_pages free pages: table
+    [B,max_pages], held [B] entries in use, free [n_pages], state [2] = the ring's
+    first place and its count; all int32."""
+    torch = _torch()
+    i32 = dict(dtype=torch.int32, device=device)
+    return {"table": torch.full((B, max_pages), -1, **i32), "held": torch.zeros(B, **i32),
+            "free": torch.arange(n_pages, **i32), "state": torch.tensor([0, n_pages], **i32)}
+
+
+def cache_pages(pool, length, page, shared=None, out=None, workspace=None, stream=None):
+    """Give every sequence the pages that length [B] int32 tokens need: a sequence that
+    grows takes pages from the head of the ring, in sequence order, one that shrinks gives
+    its last ones back behind the ring's end, where later calls find them.  shared [B]:
+    the first shared[b] entries belong to others and are never given back.  pool: as from
+    page_pool, changed in place; with out = {"table", "held", "state"} these are written
+    instead, and of pool only free[...] behind the ring's end.  Returns room [B] int32,
+    the tokens that a sequence has pages for: less than length where the ring had too few
+    (nothing of it has changed then), -1 where its length, held or shared is out of range,
+    or the ring's state is."""
+    if stream is not None:
+        return _on(stream, length, cache_pages, pool, length, page, shared, out, workspace)
+    torch = _torch()
+    i32 = torch.int32
+    table = pool["table"]
+    dev = _device_of(table, "pool table")
+    if table.dim() != 2 or pool["free"].dim() != 1:
+        raise ValueError("pool table must be [B,max_pages] and pool free [n_pages]")
+    B, mp = table.shape
+    n = pool["free"].shape[0]
+    to = pool if out is None else out
+    p, o = ([_ptr(d[k], what + " " + k, dev, i32, s)
+             for k, s in (("state", (2,)), ("held", (B,)), ("table", (B, mp)))]
+            for d, what in ((pool, "pool"), (to, "out")))
+    if workspace is None:
+        # the results and the plan in one allocation
+        both = torch.empty((4 * B + 255) // 256 * 256 + svd_cache_pages_workspace_bytes(B),
+                           dtype=torch.uint8, device=table.device)
+        room = both[:4 * B].view(i32)
+        ws, ws_bytes = both.data_ptr() + (4 * B + 255) // 256 * 256, both.numel()
+        ws_bytes -= (4 * B + 255) // 256 * 256
+    else:
+        room = torch.empty(B, dtype=i32, device=table.device)
+        ws, ws_bytes = _workspace(workspace, dev)
+    _call(_c.svd_cache_pages, "svd_cache_pages", dev, _ptr(length, "length", dev, i32, (B,)),
+          _ptr(shared, "shared", dev, i32, (B,)), B, mp, page, n,
+          _ptr(pool["free"], "pool free", dev, i32, (n,)), *p, *o, room.data_ptr(), ws, ws_bytes)
+    return room
+
+
+def cache_slots(cache, block_table, ctx_len, n_new, n, stream=None):
+    """Where packed tokens go: sequence b brings n_new[b] tokens behind its ctx_len[b], the
+    sequences one after another in n places.  Returns row_off [B+1] int32, where each
+    sequence begins, and for every place seq, pos [n] int32 and slot [n] int64, the
+    token's sequence, its position, and page * (tokens a page) + place, for
+    cache_write_slots; all -1 behind the last token, slot alone where a position has no
+    page."""
+    if stream is not None:
+        return _on(stream, block_table, cache_slots, cache, block_table, ctx_len, n_new, n)
+    torch = _torch()
+    i32 = torch.int32
+    dev = _device_of(block_table, "block_table")
+    if block_table.dim() != 2 or cache["k"].dim() != 4:
+        raise ValueError("block_table must be [B,max_pages], cache k [n_pages,kv_heads,page,D]")
+    B, mp = block_table.shape
+    n_pages, _, page, _ = cache["k"].shape
+    # one allocation: slot, then seq, pos, row_off
+    flat = torch.empty(max(n + (2 * n + B + 2) // 2, 0), dtype=torch.int64, device=block_table.device)
+    at = flat.data_ptr()
+    _call(_c.svd_cache_slots, "svd_cache_slots", dev, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
+          _ptr(n_new, "n_new", dev, i32, (B,)), _ptr(block_table, "block_table", dev, i32, (B, mp)),
+          B, mp, page, n_pages, n, at + 16 * n, at + 8 * n, at + 12 * n, at)
+    view = flat.view(i32).as_strided
+    return {"row_off": view((B + 1,), (1,), 4 * n), "seq": view((n,), (1,), 2 * n),
+            "pos": view((n,), (1,), 3 * n), "slot": flat[:n]}
+
+
+def _packed(t, name, heads, D, dev):
+    """Elements between the tokens of t [n,heads,D], whose heads are contiguous."""
+    if t.dim() != 3:
+        raise ValueError("%s must be [n,%d,%d], got %s" % (name, heads, D, list(t.shape)))
+    return _tokens(t.unsqueeze(0), name, heads, D, dev)
+
+
+def cache_write_slots(cache, k, v, slot, stream=None):
+    """Write packed k, v [n,kv_heads,D] (bf16 or fp32; the tokens may be strided) to slot
+    [n] int64, as from cache_slots; a slot outside the pages is skipped."""
+    if stream is not None:
+        return _on(stream, k, cache_write_slots, cache, k, v, slot)
+    torch = _torch()
+    c, dev = _cache_struct(cache, None, 0)
+    ks = _packed(k, "k", c.kv_heads, c.head_dim, dev)
+    vs = _packed(v, "v", c.kv_heads, c.head_dim, dev)
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must share one shape and dtype")
+    n = k.shape[0]
+    _call(_c.svd_cache_write_slots, "svd_cache_write_slots", dev, ctypes.addressof(c),
+          k.data_ptr(), v.data_ptr(), _dtype_code(k), ks, vs,
+          _ptr(slot, "slot", dev, torch.int64, (n,)), n)
+
+
+def _filter_args(logits, n_rows, temperature, top_k, top_p, min_p):
+    """(device, pointers and sizes of a filter or sample call up to min_p)."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B,T,V]")
+    dev = _device_of(logits, "logits")
+    B, T, V = logits.shape
+    b = (B,)
+    return (dev, _ptr(logits, "logits", dev, logits.dtype, logits.shape), _dtype_code(logits),
+            (B, T, V), (_ptr(n_rows, "n_rows", dev, i32, b),
+                        _ptr(temperature, "temperature", dev, f32, b),
+                        _ptr(top_k, "top_k", dev, i32, b), _ptr(top_p, "top_p", dev, f32, b),
+                        _ptr(min_p, "min_p", dev, f32, b)))
+
+
+def filter_logits(logits, temperature=None, top_k=None, top_p=None, min_p=None, n_rows=None,
+                  out=None, stream=None):
+    """logits [B,T,V] (bf16 or fp32) with -inf for the tokens that a prefix's settings drop:
+    with weights exp((z - max z) / temperature), min_p keeps those of at least min_p, top_k
+    the first top_k of them by falling logit (the lower index first among equal ones; 0 or
+    less: all), top_p the shortest beginning of that order that holds top_p of their
+    weight.  temperature, top_p, min_p [B] fp32, top_k [B] int32, each or None; a
+    temperature of 0 keeps the first most likely token alone.  The logits themselves are
+    not divided by the temperature.  n_rows [B]: rows from n_rows[b] on are left as out has
+    them.  out: default a new tensor; logits itself for a change in place.  Returns out."""
+    if stream is not None:
+        return _on(stream, logits, filter_logits, logits, temperature, top_k, top_p, min_p, n_rows,
+                   out)
+    dev, z, code, (B, T, V), ask = _filter_args(logits, n_rows, temperature, top_k, top_p, min_p)
+    if out is None:
+        out = _torch().empty_like(logits)
+    _call(_c.svd_filter_logits, "svd_filter_logits", dev, z,
+          _ptr(out, "out", dev, logits.dtype, logits.shape), code, B, T, V, *ask)
+    return out
+
+
+def sample(logits, uniforms=None, K=1, temperature=None, top_k=None, top_p=None, min_p=None,
+           n_rows=None, seed=0, row_base=0, token=None, logprob=None, want_logprob=False,
+           stream=None):
+    """K tokens from every row of logits [B,T,V], among those that filter_logits keeps, by
+    the softmax at the temperature: the first token, by index, up to which the kept
+    weights exceed uniforms times their sum.  uniforms [B,K,T] fp64 in [0,1) (K follows
+    from it); None: the library's counter hash of seed, row_base + b and k * T + t.
+    Returns token [B,K,T] int32 (-1 for a row without an answer) and, when asked for or
+    given, logprob [B,K,T] fp32, the logarithm of the token's share of the kept weight;
+    rows from n_rows[b] on are left as token and logprob have them."""
+    if stream is not None:
+        return _on(stream, logits, sample, logits, uniforms, K, temperature, top_k, top_p, min_p,
+                   n_rows, seed, row_base, token, logprob, want_logprob)
+    torch = _torch()
+    dev, z, code, (B, T, V), ask = _filter_args(logits, n_rows, temperature, top_k, top_p, min_p)
+    if uniforms is not None:
+        if uniforms.dim() != 3:
+            raise ValueError("uniforms must be [B,K,T]")
+        K = uniforms.shape[1]
+    shape = (B, K, T)
+    if token is None:
+        token = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    if logprob is None and want_logprob:
+        logprob = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    _call(_c.svd_sample, "svd_sample", dev, z, code, B, T, V, K, *ask,
+          _ptr(uniforms, "uniforms", dev, torch.float64, shape), int(seed) & _M64,
+          int(row_base) & _M64, _ptr(token, "token", dev, torch.int32, shape),
+          _ptr(logprob, "logprob", dev, torch.float32, shape))
+    return {"token": token, "logprob": logprob}
+
+
+def prefix_attention_workspace(B, T, q_heads, cache, block_table, n_groups=0):
+    """A workspace for prefix_attention calls of these sizes."""
+    torch = _torch()
+    k = cache["k"]
+    n = svd_prefix_attention_workspace_bytes(B, T, q_heads, k.shape[1], k.shape[3],
+                                             block_table.shape[1] * k.shape[2], n_groups)
+    if n == 0:
+        raise ValueError("sizes out of range: B=%d T=%d q_heads=%d cache %s groups=%d" %
+                         (B, T, q_heads, list(k.shape), n_groups))
+    return torch.empty(n, dtype=torch.uint8, device=k.device)
+
+
+def prefix_attention(q, cache, block_table, ctx_len, share_off=None, anc=None, n_nodes=None,
+                     depth=None, scale=None, cap=0.0, slopes=None, out=None, lse=None,
+                     want_lse=False, workspace=None, stream=None):
+    """tree_attention for batches that share prefixes, and for scores that are capped or
+    fall off with distance.  share_off [groups+1] int32: sequences share_off[g] to
+    share_off[g+1] - 1 are a group, and the pages that all of their block tables begin
+    with are read once for the group; what is computed does not depend on it.  cap: scores
+    become cap * tanh(score / cap) (0 or None: as they are).  slopes [q_heads] fp32: a
+    score loses slopes[h] times the distance between the two positions, a node's position
+    being ctx_len[b] + its depth (depth [B,T] int32, needed with anc).  The rest as for
+    tree_attention."""
+    if stream is not None:
+        return _on(stream, q, prefix_attention, q, cache, block_table, ctx_len, share_off, anc,
+                   n_nodes, depth, scale, cap, slopes, out, lse, want_lse, workspace)
+    torch = _torch()
+    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
+    if q.dtype != bf16:
+        raise TypeError("q must be bfloat16, got %s" % q.dtype)
+    if q.dim() != 4:
+        raise ValueError("q must be [B,T,q_heads,D]")
+    B, T, Hq, D = q.shape
+    c, dev = _cache_struct(cache, block_table, B)
+    qs = _tokens(q, "q", Hq, c.head_dim, dev)
+    if Hq % c.kv_heads != 0:
+        raise ValueError("q_heads must be a multiple of the cache's kv_heads")
+    G = 0
+    if share_off is not None:
+        if share_off.dim() != 1 or share_off.shape[0] < 2:
+            raise ValueError("share_off must be [groups+1]")
+        G = share_off.shape[0] - 1
+    if slopes is not None and anc is not None and depth is None:
+        raise ValueError("slopes over a tree need its depth")
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=bf16, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((B, T, Hq), dtype=f32, device=dev)
+    if workspace is None:
+        workspace = prefix_attention_workspace(B, T, Hq, cache, block_table, G)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call(_c.svd_prefix_attention, "svd_prefix_attention", dev, ctypes.addressof(c),
+          q.data_ptr(), qs, _ptr(ctx_len, "ctx_len", dev, i32, (B,)),
+          _ptr(n_nodes, "n_nodes", dev, i32, (B,)),
+          _ptr(anc, "anc", dev, i32, (B, T, (T + 31) // 32)),
+          _ptr(depth, "depth", dev, i32, (B, T)), _ptr(share_off, "share_off", dev, i32, (G + 1,)),
+          G, D ** -0.5 if scale is None else scale, cap or 0.0,
+          _ptr(slopes, "slopes", dev, f32, (Hq,)), B, T, Hq,
+          _ptr(out, "out", dev, bf16, (B, T, Hq, D)), _ptr(lse, "lse", dev, f32, (B, T, Hq)), ws,
+          ws_bytes)
+    return {"out": out, "lse": lse}

@@ -64,6 +64,16 @@ constexpr int kAttnLoaders = 256;   // threads that bring tiles to LDS
 constexpr int kAttnJoinBlock = 256;
 constexpr int kAttnMaxSplits = 64;
 
+// Sequences lo .. hi - 1 of a batch whose first `tokens` cached tokens are in the same pages,
+// those of sequence `first`.  tokens is a multiple of kShareTokens.
+constexpr int kShareTokens = 128;
+struct ShareGroup {
+  int32_t lo, hi, first, tokens;
+};
+struct ShareTile {          // rows of a group that one workgroup takes
+  int32_t group, row;       // group -1: none
+};
+
 struct AttnArgs {
   const uint16_t *q;        // [B][T][Hq][D] bf16, q_stride elements between tokens
   int64_t q_stride;
@@ -77,6 +87,14 @@ struct AttnArgs {
   float *part_o;            // [S][B][T][Hq][D] when S > 1
   float *part_ms;           // [S][B][T][Hq][2]
   int64_t rows_all;         // B * T * Hq
+  int parts, part0;         // parts of a row in all, and before this kernel's
+  // scores that are capped or fall off with distance, and shared prefixes (kForm)
+  float cap_in, cap_out;    // 2 log2(e) scale / cap and cap * log2(e); 0: no cap
+  const float *slopes;      // [Hq] or null
+  const int32_t *depth;     // [B][T] or null: a chain
+  const int32_t *eff;       // [B] tokens that the shared parts cover, or null
+  const ShareGroup *groups;
+  const ShareTile *tiles;
 };
 
 __device__ __forceinline__ f32x4 mfma_bf16(const vec16 &a, const vec16 &b, const f32x4 &c) {
@@ -109,6 +127,12 @@ __device__ __forceinline__ float row_max(float x) {
 // either, and its NaN sum has to stay.
 __device__ __forceinline__ float part_factor(float m, float l, float mm) {
   return m == kNegInf ? (l == 0.0f ? 0.0f : 1.0f) : fast_exp2(m - mm);
+}
+
+// cap * tanh(scale * z / cap) as a base-2 logarithm: tanh(x) = 1 - 2 / (1 + exp(2 x)).  Its
+// error is that of the subtraction from 1, 2^-24 of the cap.
+__device__ __forceinline__ float capped(float z, float in, float out) {
+  return __builtin_fmaf(-2.0f * out, __builtin_amdgcn_rcpf(1.0f + fast_exp2(z * in)), out);
 }
 
 // Whether a prefix's lengths are out of range.
@@ -169,10 +193,17 @@ struct AttnShape {
   static constexpr int kLdsBytes = 2 * kTileBytes > kJoinBytes ? 2 * kTileBytes : kJoinBytes;
 };
 
-template <int D, bool kE4M3, int NT, int WQ, int WT>
+// What a kernel computes: a prefix's rows over all of its tokens; the same behind the
+// tokens that a group shares (none without groups), with shaped scores; or a group's rows,
+// of all of its sequences, over the tokens that they share.
+enum AttnForm { kTree = 0, kShaped = 1, kShared = 2, kSharedShaped = 3 };
+
+template <int D, bool kE4M3, int NT, int WQ, int WT, int kForm>
 __global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
                              (AttnShape<D, kE4M3, NT, WQ, WT>::kMinWaves))
 void kr_tree_attention(CacheView cv, AttnArgs a) {
+  constexpr bool kRows = kForm == kShared || kForm == kSharedShaped;
+  constexpr bool kShape = kForm == kShaped || kForm == kSharedShaped;
   using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
   constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
   constexpr bool kRoles = Shape::kRoles;
@@ -193,19 +224,44 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // units on neighbouring blocks run on different XCDs; the row tiles of one
   // unit, which read the same keys and values, stay on one
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  const int unit = (idx / a.m_tiles) * 8 + xcd, mt = idx % a.m_tiles;
+  int unit = (idx / a.m_tiles) * 8 + xcd, mt = idx % a.m_tiles;
+  if (kRows && (a.units & 7)) {  // few units of many rows: on all XCDs, wherever they read
+    unit = blockIdx.x % a.units;
+    mt = blockIdx.x / a.units;
+    if (mt >= a.m_tiles) return;
+  }
   if (unit >= a.units) return;
   const int s = unit % a.S, bh = unit / a.S;
   const int h = bh % cv.Hkv;
-  const int64_t b = bh / cv.Hkv;
   const int Hq = cv.Hkv * a.group;
-  const int ctx = a.ctx_len[b];
-  const int nodes = a.n_nodes ? a.n_nodes[b] : a.T;
-  // lengths out of range: every row of the prefix is NaN
-  const bool bad = attn_bad(ctx, nodes, a.T, a.room);
-  const int rows = (bad ? a.T : nodes) * a.group;
-  const int r_lo = mt * a.m_rows, r_hi = min(r_lo + a.m_rows, rows);  // this workgroup's rows
+  int64_t b = bh / cv.Hkv;  // whose pages are read
+  int ctx, nodes, rows, r_lo, b_lo = 0;
+  bool bad = false;
+  if constexpr (kRows) {
+    const ShareTile st = a.tiles[mt];
+    if (st.group < 0) return;
+    const ShareGroup sg = a.groups[st.group];
+    if (sg.tokens == 0) return;
+    b = sg.first;
+    b_lo = sg.lo;
+    ctx = sg.tokens;
+    nodes = 0;
+    rows = (sg.hi - sg.lo) * a.T * a.group;
+    r_lo = st.row;
+  } else {
+    ctx = a.ctx_len[b];
+    nodes = a.n_nodes ? a.n_nodes[b] : a.T;
+    // lengths out of range: every row of the prefix is NaN
+    bad = attn_bad(ctx, nodes, a.T, a.room);
+    rows = (bad ? a.T : nodes) * a.group;
+    r_lo = mt * a.m_rows;
+  }
+  const int r_hi = min(r_lo + a.m_rows, rows);  // this workgroup's rows
   if (r_lo >= r_hi) return;
+  // a row's token among the batch's B * T, its node and its query head in the group
+  auto token_of = [&](int R) -> int64_t {
+    return kRows ? (int64_t)b_lo * a.T + R / a.group : b * a.T + R / a.group;
+  };
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int W = (a.T + 31) / 32;
@@ -213,8 +269,9 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   const int total = bad ? 0 : ctx + nodes;
   // a sequence's room goes up to 2^31 - page: sums past its length are 64 bits
   const int all_tiles = (int)(((int64_t)total + TK - 1) / TK);
-  const int per = (all_tiles + a.S - 1) / a.S;
-  const int t_lo = s * per, t_hi = min(t_lo + per, all_tiles);
+  const int first = kForm == kShaped && a.eff && !bad ? a.eff[b] / TK : 0;
+  const int per = (all_tiles - first + a.S - 1) / a.S;
+  const int t_lo = first + s * per, t_hi = min(t_lo + per, all_tiles);
 
   if (threadIdx.x == 0) lds_odd = 0;
   __syncthreads();
@@ -297,7 +354,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // registers to LDS.  A token without a valid page gets NaN keys, so that every row
   // that attends to it is NaN; values behind the end are zero.
   auto store_tile = [&](const Staged &st, int tile) {
-    const bool last = (int64_t)tile * TK + TK > ctx;  // holds nodes or the end
+    const bool last = !kRows && (int64_t)tile * TK + TK > ctx;  // holds nodes or the end
     vec16 *const lk = reinterpret_cast<vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
@@ -386,13 +443,23 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   auto compute = [&](auto &&before, auto &&begin, auto &&end) {
   const int wq = wave % WQ, wt = wave / WQ;
   vec16 qf[NT][ST];
-  int node[NT];
+  int node[NT], pos[NT];  // a row's node, and its position where scores fall off with distance
+  float slope[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = min(r_lo + (wq * NT + t) * 16 + n, r_hi - 1);
+    const int64_t token = token_of(r);
     node[t] = r / a.group;
-    const uint16_t *q = a.q + (b * a.T + node[t]) * a.q_stride +
-                        (int64_t)(h * a.group + r % a.group) * D;
+    const uint16_t *q = a.q + token * a.q_stride + (int64_t)(h * a.group + r % a.group) * D;
+    if constexpr (kShape) {
+      pos[t] = 0;
+      slope[t] = 0.0f;
+      if (a.slopes) {
+        const int64_t rb = token / a.T;
+        pos[t] = a.ctx_len[rb] + (a.depth ? a.depth[token] : (int)(token % a.T));
+        slope[t] = a.slopes[h * a.group + r % a.group] * 1.4426950408889634f;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < ST; ++i) qf[t][i] = *reinterpret_cast<const vec16 *>(q + 32 * i + 8 * g);
   }
@@ -407,11 +474,12 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  const float cs = kShape ? 1.0f : a.c;  // shaped scores are base-2 logarithms already
   const int steps = (t_hi - t_lo + PF - 1) / PF * PF;  // as the loading waves take
   if (t_lo < t_hi) before();
   for (int tile = t_lo; tile < t_lo + steps; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
-    const bool last = p0 + TK > ctx;  // holds nodes or the end
+    const bool last = !kRows && p0 + TK > ctx;  // holds nodes or the end
     const vec16 *const lk =
         reinterpret_cast<const vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     const unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
@@ -434,6 +502,40 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) sc[t][u] = mfma_bf16(kf, qf[t][i], sc[t][u]);
           }
+        if constexpr (kShape) {
+          // to base-2 logarithms: capped, then less what the distance takes
+          if (a.cap_in > 0.0f) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int u = 0; u < G / 16; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sc[t][u][r] = capped(sc[t][u][r], a.cap_in, a.cap_out);
+          } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int u = 0; u < G / 16; ++u) sc[t][u] *= a.c;
+          }
+          if (a.slopes) {
+            const int at = (int)(p0 + k0) + 4 * g;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const float from = (float)(at - pos[t]);
+#pragma unroll
+              for (int u = 0; u < G / 16; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  float far = from + (float)(16 * u + r);
+                  if (last && a.depth) {
+                    const int i = at + 16 * u + r - ctx;
+                    if (i >= 0 && i < nodes) far = (float)(ctx + a.depth[b * a.T + i] - pos[t]);
+                  }
+                  sc[t][u][r] = __builtin_fmaf(slope[t], far, sc[t][u][r]);
+                }
+            }
+          }
+        }
         if (last) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -462,7 +564,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
           for (int u = 0; u < G / 16; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[t][u][r]);
-          next[t] = row_max(mx) * a.c;
+          next[t] = row_max(mx) * cs;
           moves |= next[t] > base[t] + 8.0f;
         }
         if (__any(moves)) {
@@ -484,7 +586,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
           for (int u = 0; u < G / 16; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              sc[t][u][r] = fast_exp2(__builtin_fmaf(sc[t][u][r], a.c, -sub));
+              sc[t][u][r] = fast_exp2(__builtin_fmaf(sc[t][u][r], cs, -sub));
               l[t] += sc[t][u][r];
             }
 #pragma unroll
@@ -579,9 +681,9 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 
   // one row's 4 elements from d on, its exponent and its sum
   auto put = [&](int R, int d, f32x4 x, float mm, float ll, bool first) {
-    const int64_t row = (b * a.T + R / a.group) * Hq + h * a.group + R % a.group;
-    if (a.S > 1) {
-      const int64_t pr = (int64_t)s * a.rows_all + row;
+    const int64_t row = token_of(R) * Hq + h * a.group + R % a.group;
+    if (a.parts > 1) {
+      const int64_t pr = (int64_t)(a.part0 + s) * a.rows_all + row;
       *reinterpret_cast<f32x4 *>(a.part_o + pr * D + d) = x;
       if (first) {
         a.part_ms[2 * pr] = mm;
@@ -617,7 +719,21 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       float z = 0.0f;
       for (int e = 0; e < D; ++e)
         z += cache_element<kE4M3, D>(cv.k, cv.k_scale, row, e) * BF16::at(q, e);
-      const float pt = fast_exp2(__builtin_fmaf(z, a.c, -(mm == kNegInf ? 0.0f : mm)));
+      const float sub = mm == kNegInf ? 0.0f : mm;
+      float pt;
+      if constexpr (kShape) {
+        z = a.cap_in > 0.0f ? capped(z, a.cap_in, a.cap_out) : z * a.c;
+        if (a.slopes) {
+          const int64_t token = b * a.T + nd;
+          const int to = ctx + (a.depth ? a.depth[token] : nd);
+          const int from = i >= 0 && a.depth ? ctx + a.depth[b * a.T + i] : (int)p;
+          z = __builtin_fmaf(a.slopes[h * a.group + R % a.group] * 1.4426950408889634f,
+                             (float)(from - to), z);
+        }
+        pt = fast_exp2(z - sub);
+      } else {
+        pt = fast_exp2(__builtin_fmaf(z, a.c, -sub));
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (!(fabsf(v[e]) < __builtin_huge_valf())) x[e] += pt * v[e];
@@ -640,7 +756,8 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       ll += lds_ms[w][r][1] * f;
       x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
     }
-    if (lds_odd) x = odd_values(r_lo + r, d, x, mm);
+    if constexpr (!kRows)
+      if (lds_odd) x = odd_values(r_lo + r, d, x, mm);
     put(r_lo + r, d, x, mm, ll, d == 0);
   }
 }
@@ -657,13 +774,15 @@ __global__ __launch_bounds__(kAttnJoinBlock) void kr_attn_join(AttnArgs a, int H
   const int nodes = a.n_nodes ? a.n_nodes[b] : a.T;
   // a prefix out of range wrote NaN parts for every row
   if (bt % a.T >= nodes && !attn_bad(a.ctx_len[b], nodes, a.T, a.room)) return;
+  // a sequence that shares nothing has no shared parts
+  const int s0 = a.eff && a.eff[b] == 0 ? a.part0 : 0;
   float m = kNegInf;
 #pragma unroll 8
-  for (int s = 0; s < a.S; ++s) m = fmaxf(m, a.part_ms[2 * (s * a.rows_all + row)]);
+  for (int s = s0; s < a.parts; ++s) m = fmaxf(m, a.part_ms[2 * (s * a.rows_all + row)]);
   float l = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-  for (int s = 0; s < a.S; ++s) {
+  for (int s = s0; s < a.parts; ++s) {
     const int64_t pr = s * a.rows_all + row;
     const float ms = a.part_ms[2 * pr], ls = a.part_ms[2 * pr + 1];
     const float f = part_factor(ms, ls, m);

@@ -78,40 +78,11 @@ __device__ __forceinline__ void load8(const typename E::elem *p, float *x) {
   }
 }
 
-// k and v rows of B x T tokens into the cache.  L = D / 8 lanes per (token,
-// head, k or v) row; blocks_per_b workgroups per sequence.
-template <typename E, bool kVec, bool kE4M3, int D>
-__global__ __launch_bounds__(kCacheBlock) void kr_cache_write(
-    const typename E::elem *__restrict__ k, const typename E::elem *__restrict__ v,
-    int64_t k_stride, int64_t v_stride, const int32_t *__restrict__ ctx_len,
-    const int32_t *__restrict__ n_new, const int32_t *__restrict__ dst, int64_t T,
-    int64_t blocks_per_b, CacheView c) {
-  constexpr int L = D / 8, kRows = kCacheBlock / L;
-  const int64_t b = blockIdx.x / blocks_per_b;
-  const int64_t row = (blockIdx.x % blocks_per_b) * kRows + threadIdx.x / L;
-  const int lane = threadIdx.x % L;
-  const int64_t rows = T * c.Hkv * 2;
-  if (row >= rows) return;
-  // v rows behind the k rows of a token
-  const int hv = (int)(row % (2 * c.Hkv));
-  const int64_t t = row / (2 * c.Hkv);
-  const bool is_v = hv >= c.Hkv;
-  const int h = is_v ? hv - c.Hkv : hv;
-  const int n = n_new ? n_new[b] : (int)T;
-  if (t >= n) return;
-  int64_t at = t;
-  if (dst) {
-    at = dst[b * T + t];
-    if (at < 0) return;
-  }
-  const int64_t ctx = ctx_len[b];
-  if (ctx < 0) return;
-  const int64_t to = cache_row(c, b, ctx + at, h);
-  if (to < 0) return;
-  const typename E::elem *src = (is_v ? v + (b * T + t) * v_stride : k + (b * T + t) * k_stride) +
-                                (int64_t)h * D + lane * 8;
-  float x[8];
-  load8<E, kVec>(src, x);
+// One lane's 8 elements of a cached row: all L lanes of the row take part.
+template <bool kE4M3, int D>
+__device__ __forceinline__ void store_row8(const CacheView &c, bool is_v, int64_t to, int lane,
+                                           float (&x)[8]) {
+  constexpr int L = D / 8;
   uint8_t *out = is_v ? c.v : c.k;
   if constexpr (!kE4M3) {
     vec16 w;
@@ -152,6 +123,68 @@ __global__ __launch_bounds__(kCacheBlock) void kr_cache_write(
     *reinterpret_cast<uint2 *>(out + to * D + lane * 8) = w;
     if (lane == 0) (is_v ? c.v_scale : c.k_scale)[to] = (uint8_t)byte;
   }
+}
+
+// k and v rows of B x T tokens into the cache.  L = D / 8 lanes per (token,
+// head, k or v) row; blocks_per_b workgroups per sequence.
+template <typename E, bool kVec, bool kE4M3, int D>
+__global__ __launch_bounds__(kCacheBlock) void kr_cache_write(
+    const typename E::elem *__restrict__ k, const typename E::elem *__restrict__ v,
+    int64_t k_stride, int64_t v_stride, const int32_t *__restrict__ ctx_len,
+    const int32_t *__restrict__ n_new, const int32_t *__restrict__ dst, int64_t T,
+    int64_t blocks_per_b, CacheView c) {
+  constexpr int L = D / 8, kRows = kCacheBlock / L;
+  const int64_t b = blockIdx.x / blocks_per_b;
+  const int64_t row = (blockIdx.x % blocks_per_b) * kRows + threadIdx.x / L;
+  const int lane = threadIdx.x % L;
+  const int64_t rows = T * c.Hkv * 2;
+  if (row >= rows) return;
+  // v rows behind the k rows of a token
+  const int hv = (int)(row % (2 * c.Hkv));
+  const int64_t t = row / (2 * c.Hkv);
+  const bool is_v = hv >= c.Hkv;
+  const int h = is_v ? hv - c.Hkv : hv;
+  const int n = n_new ? n_new[b] : (int)T;
+  if (t >= n) return;
+  int64_t at = t;
+  if (dst) {
+    at = dst[b * T + t];
+    if (at < 0) return;
+  }
+  const int64_t ctx = ctx_len[b];
+  if (ctx < 0) return;
+  const int64_t to = cache_row(c, b, ctx + at, h);
+  if (to < 0) return;
+  const typename E::elem *src = (is_v ? v + (b * T + t) * v_stride : k + (b * T + t) * k_stride) +
+                                (int64_t)h * D + lane * 8;
+  float x[8];
+  load8<E, kVec>(src, x);
+  store_row8<kE4M3, D>(c, is_v, to, lane, x);
+}
+
+// The same for N packed tokens, each to a slot of its own: page * n + place with n tokens a
+// page.  A slot outside the pages is not written.
+template <typename E, bool kVec, bool kE4M3, int D>
+__global__ __launch_bounds__(kCacheBlock) void kr_cache_write_slots(
+    const typename E::elem *__restrict__ k, const typename E::elem *__restrict__ v,
+    int64_t k_stride, int64_t v_stride, const int64_t *__restrict__ slots, int64_t N, CacheView c) {
+  constexpr int L = D / 8, kRows = kCacheBlock / L;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+  const int lane = threadIdx.x % L;
+  if (row >= N * c.Hkv * 2) return;
+  const int hv = (int)(row % (2 * c.Hkv));
+  const int64_t t = row / (2 * c.Hkv);
+  const bool is_v = hv >= c.Hkv;
+  const int h = is_v ? hv - c.Hkv : hv;
+  const int64_t slot = slots[t];
+  if (slot < 0 || slot >> c.page_shift >= c.n_pages) return;
+  const int64_t to = (((slot >> c.page_shift) * c.Hkv + h) << c.page_shift) +
+                     (slot & ((1 << c.page_shift) - 1));
+  const typename E::elem *src =
+      (is_v ? v + t * v_stride : k + t * k_stride) + (int64_t)h * D + lane * 8;
+  float x[8];
+  load8<E, kVec>(src, x);
+  store_row8<kE4M3, D>(c, is_v, to, lane, x);
 }
 
 // Positions start[b] .. start[b] + count[b] - 1 of every sequence, widened to

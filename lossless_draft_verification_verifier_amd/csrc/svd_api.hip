@@ -19,9 +19,12 @@
 #include "kr_cache.hpp"
 #include "kr_cps.hpp"
 #include "kr_draw.hpp"
+#include "kr_filter.hpp"
+#include "kr_pages.hpp"
 #include "kr_rows.hpp"
 #include "kr_rowstats.hpp"
 #include "kr_select.hpp"
+#include "kr_share.hpp"
 #include "kr_tree.hpp"
 
 namespace {
@@ -857,3 +860,4 @@ const char *svd_strerror(int status) {
 }  // extern "C"
 
 #include "svd_step.hpp"
+#include "svd_serve.hpp"

@@ -15,8 +15,8 @@ bool tree_sizes_ok(int64_t B, int32_t T) {
 }
 
 // The cache's arrays and sizes; fills the view.
-int cache_view(const svd_cache_t *c, CacheView &v) {
-  if (!c || !c->k || !c->v || !c->block_table) return SVD_EINVAL;
+int cache_view(const svd_cache_t *c, CacheView &v, bool table = true) {
+  if (!c || !c->k || !c->v || (table && !c->block_table)) return SVD_EINVAL;
   if (c->dtype != SVD_CACHE_BF16 && c->dtype != SVD_CACHE_E4M3) return SVD_EDTYPE;
   const bool e4m3 = c->dtype == SVD_CACHE_E4M3;
   if (e4m3 && (!c->k_scale || !c->v_scale)) return SVD_EINVAL;
@@ -25,10 +25,10 @@ int cache_view(const svd_cache_t *c, CacheView &v) {
     return SVD_EINVAL;
   if (c->head_dim != 64 && c->head_dim != 128) return SVD_EINVAL;
   if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1)) != 0) return SVD_EINVAL;
-  if (c->n_pages < 1 || c->n_pages >= (int64_t)1 << 31 || c->max_pages < 1 || c->kv_heads < 1 ||
-      c->kv_heads > 4096)
+  if (c->n_pages < 1 || c->n_pages >= (int64_t)1 << 31 || c->kv_heads < 1 || c->kv_heads > 4096)
     return SVD_EINVAL;
-  if ((int64_t)c->max_pages * c->page >= (int64_t)1 << 31) return SVD_EINVAL;
+  if (table && (c->max_pages < 1 || (int64_t)c->max_pages * c->page >= (int64_t)1 << 31))
+    return SVD_EINVAL;
   if (((uintptr_t)c->k) % 16 != 0 || ((uintptr_t)c->v) % 16 != 0) return SVD_EINVAL;
   v.k = static_cast<uint8_t *>(c->k);
   v.v = static_cast<uint8_t *>(c->v);
@@ -147,17 +147,69 @@ bool attn_sizes_ok(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int
          grid_ok(((B * Hkv * p.S + 7) / 8 * 8) * p.m_tiles, threads);
 }
 
+// Pointers, sizes and scale of an attention call; cs: scale * log2(e).
+int attn_check(const CacheView &c, int D, const void *q, int64_t q_stride, const int32_t *ctx_len,
+               float scale, int64_t B, int32_t T, int32_t q_heads, const void *out,
+               const void *workspace, float &cs) {
+  if (!q || !ctx_len || !out || !workspace) return SVD_EINVAL;
+  const int64_t room = (int64_t)c.max_pages << c.page_shift;
+  if (!attn_sizes_ok(B, T, q_heads, c.Hkv, D, room)) return SVD_EINVAL;
+  if (!(std::isfinite(scale) && scale > 0.0f)) return SVD_EINVAL;
+  cs = (float)(1.4426950408889634 * (double)scale);
+  if (!(std::isfinite(cs) && cs > 0.0f)) return SVD_EINVAL;
+  if (q_stride < (int64_t)q_heads * D || q_stride % 8 != 0 || ((uintptr_t)q) % 16 != 0 ||
+      ((uintptr_t)out) % 16 != 0 || ((uintptr_t)workspace) % kAlign != 0)
+    return SVD_EINVAL;
+  return SVD_OK;
+}
+
+// Whether out meets the memory of q: a row with values that are not finite reads its
+// query again while pieces of its output are written already.
+bool attn_overlap(const void *q, int64_t q_stride, const void *out, int64_t tokens, uint64_t row) {
+  const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+  return q0 < o0 + (uint64_t)tokens * row &&
+         o0 < q0 + (uint64_t)(tokens - 1) * ((uint64_t)q_stride * 2) + row;
+}
+
+// What every kernel of an attention call is given.
+AttnArgs attn_args(const CacheView &c, const void *q, int64_t q_stride, const int32_t *ctx_len,
+                   const int32_t *n_nodes, const uint32_t *anc, float cs, int64_t B, int32_t T,
+                   int32_t q_heads, void *out, float *lse) {
+  AttnArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_stride = q_stride;
+  a.ctx_len = ctx_len;
+  a.n_nodes = n_nodes;
+  a.table = c.table;
+  a.anc = anc;
+  a.room = (int64_t)c.max_pages << c.page_shift;
+  a.T = T;
+  a.group = q_heads / c.Hkv;
+  a.c = cs;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.rows_all = B * T * q_heads;
+  return a;
+}
+
+void attn_split(AttnArgs &a, const AttnPlan &p, int64_t units) {
+  a.S = p.S;
+  a.m_tiles = p.m_tiles;
+  a.m_rows = p.m_rows;
+  a.units = (int)units;
+}
+
 size_t attn_ms_offset(int64_t rows, int S, int D) {
   return align_up((size_t)rows * S * D * sizeof(float));
 }
 
-template <int D, bool kE4M3, int NT, int WQ, int WT>
+template <int D, bool kE4M3, int NT, int WQ, int WT, int kForm>
 int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   CallTimer tm;
   const int64_t grid = ((int64_t)a.units + 7) / 8 * 8 * a.m_tiles;
-  SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ, WT>,
+  SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ, WT, kForm>,
              dim3((unsigned)grid), dim3(AttnShape<D, kE4M3, NT, WQ, WT>::kBlock), s, c, a);
-  if (a.S > 1) {
+  if (a.parts > 1 && a.part0 + a.S == a.parts) {  // the last of a row's parts
     constexpr int rows = kAttnJoinBlock / (D / 4);
     SVD_LAUNCH(tm, SVD_KERNEL_ATTENTION_JOIN, s, kr_attn_join<D>,
                dim3((unsigned)((a.rows_all + rows - 1) / rows)), dim3(kAttnJoinBlock), s, a, Hq);
@@ -165,14 +217,27 @@ int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   return SVD_OK;
 }
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, int kForm>
 int attn_rows(const AttnPlan &p, const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
-  if (p.nt == 2 && p.wq == 8) return attn_launch<D, kE4M3, 2, 8, 1>(c, a, Hq, s);
-  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 2>(c, a, Hq, s);
-  if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4, 1>(c, a, Hq, s);
-  if (p.wq == 3) return attn_launch<D, kE4M3, 1, 3, 1>(c, a, Hq, s);
-  if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2, 2>(c, a, Hq, s);
-  return attn_launch<D, kE4M3, 1, 1, 2>(c, a, Hq, s);
+  if (p.nt == 2 && p.wq == 8) return attn_launch<D, kE4M3, 2, 8, 1, kForm>(c, a, Hq, s);
+  if constexpr (kForm == kTree || kForm == kShaped) {  // the arrangements of a group's rows are fewer
+    if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 2, kForm>(c, a, Hq, s);
+    if (p.wq == 3) return attn_launch<D, kE4M3, 1, 3, 1, kForm>(c, a, Hq, s);
+    if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2, 2, kForm>(c, a, Hq, s);
+  }
+  if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4, 1, kForm>(c, a, Hq, s);
+  return attn_launch<D, kE4M3, 1, 1, 2, kForm>(c, a, Hq, s);
+}
+
+template <int kForm>
+int attn_kind(const svd_cache_t *cache, const AttnPlan &p, const CacheView &c, const AttnArgs &a,
+              int Hq, hipStream_t s) {
+  const int D = cache->head_dim;
+  if (cache->dtype == SVD_CACHE_E4M3)
+    return D == 64 ? attn_rows<64, true, kForm>(p, c, a, Hq, s)
+                   : attn_rows<128, true, kForm>(p, c, a, Hq, s);
+  return D == 64 ? attn_rows<64, false, kForm>(p, c, a, Hq, s)
+                 : attn_rows<128, false, kForm>(p, c, a, Hq, s);
 }
 
 template <typename E, bool kVec, bool kBias, int PATH>
@@ -275,55 +340,25 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
                        float scale, int64_t B, int32_t T, int32_t q_heads, void *out, float *lse,
                        void *workspace, size_t workspace_bytes, void *hip_stream) {
   CacheView c;
-  const int rc = cache_view(cache, c);
+  int rc = cache_view(cache, c);
   if (rc != SVD_OK) return rc;
-  if (!q || !ctx_len || !out || !workspace) return SVD_EINVAL;
   const int D = cache->head_dim;
   const int64_t room = (int64_t)c.max_pages << c.page_shift;
-  if (!attn_sizes_ok(B, T, q_heads, c.Hkv, D, room)) return SVD_EINVAL;
-  if (!(std::isfinite(scale) && scale > 0.0f)) return SVD_EINVAL;
-  const float cs = (float)(1.4426950408889634 * (double)scale);
-  if (!(std::isfinite(cs) && cs > 0.0f)) return SVD_EINVAL;
-  if (q_stride < (int64_t)q_heads * D || q_stride % 8 != 0 || ((uintptr_t)q) % 16 != 0 ||
-      ((uintptr_t)out) % 16 != 0 || ((uintptr_t)workspace) % kAlign != 0)
-    return SVD_EINVAL;
+  float cs;
+  rc = attn_check(c, D, q, q_stride, ctx_len, scale, B, T, q_heads, out, workspace, cs);
+  if (rc != SVD_OK) return rc;
   if (workspace_bytes < svd_tree_attention_workspace_bytes(B, T, q_heads, c.Hkv, D, room))
     return SVD_EWORKSPACE;
-  // a row with values that are not finite reads its query again while pieces of its
-  // output are written already
-  const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
-  const uint64_t row = (uint64_t)q_heads * D * 2;
-  if (q0 < o0 + (uint64_t)(B * T) * row &&
-      o0 < q0 + (uint64_t)(B * T - 1) * ((uint64_t)q_stride * 2) + row)
-    return SVD_EINVAL;
+  if (attn_overlap(q, q_stride, out, B * T, (uint64_t)q_heads * D * 2)) return SVD_EINVAL;
   const AttnPlan p = attn_plan(B, T, q_heads, c.Hkv, D, room);
-  AttnArgs a;
-  a.q = static_cast<const uint16_t *>(q);
-  a.q_stride = q_stride;
-  a.ctx_len = ctx_len;
-  a.n_nodes = n_nodes;
-  a.table = c.table;
-  a.anc = anc;
-  a.room = room;
-  a.T = T;
-  a.group = q_heads / c.Hkv;
-  a.S = p.S;
-  a.m_tiles = p.m_tiles;
-  a.m_rows = p.m_rows;
-  a.units = (int)(B * c.Hkv * p.S);
-  a.c = cs;
-  a.out = static_cast<uint16_t *>(out);
-  a.lse = lse;
-  a.rows_all = B * T * q_heads;
+  AttnArgs a = attn_args(c, q, q_stride, ctx_len, n_nodes, anc, cs, B, T, q_heads, out, lse);
+  attn_split(a, p, B * c.Hkv * p.S);
+  a.parts = p.S;
   a.part_o = static_cast<float *>(workspace);
   a.part_ms = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                         attn_ms_offset(a.rows_all, p.S, D));
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (cache->dtype == SVD_CACHE_E4M3)
-    return D == 64 ? attn_rows<64, true>(p, c, a, q_heads, s)
-                   : attn_rows<128, true>(p, c, a, q_heads, s);
-  return D == 64 ? attn_rows<64, false>(p, c, a, q_heads, s)
-                 : attn_rows<128, false>(p, c, a, q_heads, s);
+  return attn_kind<kTree>(cache, p, c, a, q_heads, s);
 }
 
 int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t B, int32_t T,
