@@ -22,9 +22,7 @@
 namespace svd {
 
 constexpr int kFilterBlock = 1024;
-constexpr int kFilterWaves = kFilterBlock / 64;
 constexpr int kFilterBins = 4096;   // of the first search step
-constexpr int kFilterSlabs = 1024;  // parts of a row in index order
 constexpr uint64_t kSample = 4;     // the purpose of a draw's uniforms (after kBonus)
 
 struct FilterArgs {
@@ -54,20 +52,22 @@ struct Kept {
   __device__ bool has(uint32_t k, int64_t i) const { return k > key || (k == key && i < tie); }
 };
 
+template <int NT>
 struct FilterLds {
   unsigned long long hist[kFilterBins];
-  unsigned long long slabs[kFilterSlabs];
-  unsigned long long wave[kFilterWaves + 1];
+  unsigned long long slabs[NT];
+  unsigned long long wave[NT / 64 + 1];
   unsigned long long found[4];
-  float red[kFilterWaves + 1];
+  float red[NT / 64 + 1];
   int flag;
   ExpTable tab;
 };
 
 // The sums of x over the threads before this one; total: over all of them.
-__device__ __forceinline__ unsigned long long filter_scan(unsigned long long x,
-                                                          unsigned long long &total,
-                                                          FilterLds &l) {
+template <int NT>
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long x,
+                                                         unsigned long long &total,
+                                                         unsigned long long *lds /* NT / 64 */) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   unsigned long long up = x;
 #pragma unroll
@@ -75,13 +75,13 @@ __device__ __forceinline__ unsigned long long filter_scan(unsigned long long x,
     const unsigned long long p = __shfl_up(up, off, 64);
     if (lane >= off) up += p;
   }
-  if (lane == 63) l.wave[w] = up;
+  if (lane == 63) lds[w] = up;
   __syncthreads();
   unsigned long long before = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < kFilterWaves; ++i) {
+  for (int i = 0; i < NT / 64; ++i) {
     if (i == w) before = all;
-    all += l.wave[i];
+    all += lds[i];
   }
   __syncthreads();
   total = all;
@@ -90,27 +90,27 @@ __device__ __forceinline__ unsigned long long filter_scan(unsigned long long x,
 
 // The logits of a row, visited in index order by 8 * kFilterBlock tokens at a time:
 // f(index, value) for every token.
-template <typename E, bool kVec, typename F>
+template <typename E, bool kVec, int NT, typename F>
 __device__ __forceinline__ void filter_visit(const typename E::elem *row, int64_t lo, int64_t hi,
                                              F &&f) {
   if constexpr (kVec) {
     constexpr int P = E::kPerVec;
-    for (int64_t i = lo + (int64_t)threadIdx.x * P; i < hi; i += (int64_t)kFilterBlock * P) {
+    for (int64_t i = lo + (int64_t)threadIdx.x * P; i < hi; i += (int64_t)NT * P) {
       float x[P];
       E::unpack(*reinterpret_cast<const vec16 *>(row + i), x);
 #pragma unroll
       for (int e = 0; e < P; ++e) f(i + e, x[e]);
     }
   } else {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kFilterBlock) f(i, E::at(row, i));
+    for (int64_t i = lo + threadIdx.x; i < hi; i += NT) f(i, E::at(row, i));
   }
 }
 
-template <typename E, bool kVec>
+template <typename E, bool kVec, int NT>
 struct FilterRow {
   const typename E::elem *row;
   const FilterArgs &a;
-  FilterLds &l;
+  FilterLds<NT> &l;
   float m;        // the largest logit
   double c;       // 256 log2(e) / temperature
   double unit;    // 2^shift
@@ -136,22 +136,22 @@ struct FilterRow {
 #pragma unroll
     for (int step = 0; step < kSteps; ++step) {
       const int nb = first[step], bins = 1 << nb;
-      for (int i = threadIdx.x; i < bins; i += kFilterBlock) l.hist[i] = 0;
+      for (int i = threadIdx.x; i < bins; i += NT) l.hist[i] = 0;
       __syncthreads();
-      filter_visit<E, kVec>(row, 0, a.V, [&](int64_t i, float z) {
+      filter_visit<E, kVec, NT>(row, 0, a.V, [&](int64_t i, float z) {
         const uint32_t k = logit_key(z);
         if ((bits == 0 || k >> (32 - bits) == prefix >> (32 - bits)) && take(k, i))
           atomicAdd(&l.hist[(k << bits) >> (32 - nb)], weigh(z));
       });
       __syncthreads();
       // bins by falling key, a run of them per thread
-      const int per = (bins + kFilterBlock - 1) / kFilterBlock;
+      const int per = (bins + NT - 1) / NT;
       unsigned long long mine = 0, total;
       for (int j = 0; j < per; ++j) {
         const int at = bins - 1 - ((int)threadIdx.x * per + j);
         if (at >= 0) mine += l.hist[at];
       }
-      unsigned long long upto = above + filter_scan(mine, total, l);
+      unsigned long long upto = above + block_scan<NT>(mine, total, l.wave);
       if (upto < target && upto + mine >= target) {
         for (int j = 0; j < per; ++j) {
           const int at = bins - 1 - ((int)threadIdx.x * per + j);
@@ -177,12 +177,12 @@ struct FilterRow {
   // The sums of weigh(token) over the parts of the row, in l.slabs.
   template <typename Weigh>
   __device__ void slab_sums(Weigh &&weigh) {
-    for (int i = threadIdx.x; i < kFilterSlabs; i += kFilterBlock) l.slabs[i] = 0;
+    for (int i = threadIdx.x; i < NT; i += NT) l.slabs[i] = 0;
     __syncthreads();
     int s = 0;
     for (int64_t lo = 0; lo < a.V; lo += a.slab, ++s) {
       unsigned long long sum = 0;
-      filter_visit<E, kVec>(row, lo, min(lo + a.slab, a.V),
+      filter_visit<E, kVec, NT>(row, lo, min(lo + a.slab, a.V),
                             [&](int64_t i, float z) { sum += weigh(i, z); });
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
@@ -196,10 +196,9 @@ struct FilterRow {
   template <typename Weigh>
   __device__ int64_t locate(unsigned long long target, Weigh &&weigh) {
     const int n = (int)((a.V + a.slab - 1) / a.slab);
-    static_assert(kFilterSlabs == kFilterBlock, "a part per thread");
     const unsigned long long mine = (int)threadIdx.x < n ? l.slabs[threadIdx.x] : 0;
     unsigned long long total;
-    const unsigned long long upto = filter_scan(mine, total, l);
+    const unsigned long long upto = block_scan<NT>(mine, total, l.wave);
     if (upto < target && upto + mine >= target) {
       l.found[0] = threadIdx.x;
       l.found[1] = upto;
@@ -209,7 +208,7 @@ struct FilterRow {
     unsigned long long before = l.found[1];
     __syncthreads();
     constexpr int P = 8;
-    for (int64_t lo = lo0; lo < hi0; lo += P * kFilterBlock) {
+    for (int64_t lo = lo0; lo < hi0; lo += P * NT) {
       // 8 tokens per thread
       const int64_t i0 = lo + (int64_t)threadIdx.x * P;
       unsigned long long w[P], sum = 0;
@@ -218,7 +217,7 @@ struct FilterRow {
         w[e] = i0 + e < hi0 ? weigh(i0 + e, E::at(row, i0 + e)) : 0;
         sum += w[e];
       }
-      unsigned long long at = before + filter_scan(sum, total, l);
+      unsigned long long at = before + block_scan<NT>(sum, total, l.wave);
       if (at < target && at + sum >= target) {
 #pragma unroll
         for (int e = 0; e < P; ++e) {
@@ -243,6 +242,34 @@ struct FilterRow {
   }
 };
 
+template <typename E>
+__device__ __forceinline__ void fill_nan(typename E::elem *to, int64_t V) {
+  typename E::elem nan;
+  if constexpr (sizeof(nan) == 2) nan = 0x7fc0;
+  else nan = __uint_as_float(0x7fc00000u);
+  for (int64_t i = threadIdx.x; i < V; i += blockDim.x) to[i] = nan;
+}
+
+// Draw k of row (b, t): its uniform; the sum it is drawn at, 1 to total; its outputs.
+__device__ __forceinline__ double draw_uniform(const FilterArgs &a, int64_t b, int k, int t) {
+  if (a.u) return a.u[(b * a.K + k) * a.T + t];
+  return counter_uniform(a.seed, a.row_base + (uint64_t)b,
+                         (uint64_t)k * (uint64_t)a.T + (uint64_t)t, kSample);
+}
+__device__ __forceinline__ unsigned long long draw_target(double u, unsigned long long total) {
+  const unsigned long long x = (unsigned long long)(u * (double)total);
+  return x < total ? x + 1 : total;
+}
+__device__ __forceinline__ void put_draw(const FilterArgs &a, int64_t b, int k, int t, int64_t v,
+                                         float z, float m, float temp, unsigned long long total) {
+  const int64_t at = (b * a.K + k) * a.T + t;
+  a.token[at] = (int32_t)v;
+  if (a.logprob)
+    a.logprob[at] = v < 0 ? __uint_as_float(0x7fc00000u)
+                          : (float)(((double)z - (double)m) / (double)temp -
+                                    log(ldexp((double)total, -a.shift)));
+}
+
 // What a prefix asks for, and whether a row of it has an answer.
 struct FilterAsk {
   float t, p, least;
@@ -266,21 +293,21 @@ __device__ __forceinline__ FilterAsk filter_ask(const FilterArgs &a, int64_t b) 
 }
 
 // The largest logit of a row and what it keeps; false: no answer (a NaN, +inf, or all -inf).
-template <typename E, bool kVec>
-__device__ __forceinline__ bool filter_row(FilterRow<E, kVec> &r, const FilterAsk &q, Kept &kept) {
-  FilterLds &l = r.l;
+template <typename E, bool kVec, int NT>
+__device__ __forceinline__ bool filter_row(FilterRow<E, kVec, NT> &r, const FilterAsk &q, Kept &kept) {
+  FilterLds<NT> &l = r.l;
   const FilterArgs &a = r.a;
-  exp_table_init<kFilterBlock>(l.tab);
+  exp_table_init<NT>(l.tab);
   if (threadIdx.x == 0) l.flag = 0;
   __syncthreads();
   float m = kNegInf;
   bool bad = false;
-  filter_visit<E, kVec>(r.row, 0, a.V, [&](int64_t, float z) {
+  filter_visit<E, kVec, NT>(r.row, 0, a.V, [&](int64_t, float z) {
     bad |= !(z < __builtin_huge_valf());
     m = fmaxf(m, z);
   });
   if (__any(bad) && (threadIdx.x & 63) == 0) l.flag = 1;
-  m = block_max<kFilterWaves>(m, l.red);
+  m = block_max<NT / 64>(m, l.red);
   if (l.flag || m == kNegInf) return false;
   r.m = m;
   r.c = exp2_scale(q.t);
@@ -300,8 +327,8 @@ __device__ __forceinline__ bool filter_row(FilterRow<E, kVec> &r, const FilterAs
   if (q.k > 0 && q.k < a.V) {
     // all of them when there are no more than k
     unsigned long long n = 0, total;
-    filter_visit<E, kVec>(r.row, 0, a.V, [&](int64_t, float z) { n += logit_key(z) >= least; });
-    filter_scan(n, total, l);
+    filter_visit<E, kVec, NT>(r.row, 0, a.V, [&](int64_t, float z) { n += logit_key(z) >= least; });
+    block_scan<NT>(n, total, l.wave);
     if (total > (unsigned long long)q.k) {
       uint32_t key;
       unsigned long long above;
@@ -318,10 +345,10 @@ __device__ __forceinline__ bool filter_row(FilterRow<E, kVec> &r, const FilterAs
     const Kept k0 = kept;
     auto take = [&](uint32_t k, int64_t i) { return k0.has(k, i); };
     unsigned long long sum = 0, total;
-    filter_visit<E, kVec>(r.row, 0, a.V, [&](int64_t i, float z) {
+    filter_visit<E, kVec, NT>(r.row, 0, a.V, [&](int64_t i, float z) {
       if (take(logit_key(z), i)) sum += r.weight(z);
     });
-    filter_scan(sum, total, l);
+    block_scan<NT>(sum, total, l.wave);
     const double want = ceil(fmax((double)q.p, 0.0) * (double)total);
     unsigned long long target = (unsigned long long)want;
     target = target < 1 ? 1 : target > total ? total : target;
@@ -337,31 +364,24 @@ __device__ __forceinline__ bool filter_row(FilterRow<E, kVec> &r, const FilterAs
   return true;
 }
 
-template <typename E, bool kVec>
-__global__ __launch_bounds__(kFilterBlock) void kr_filter(const typename E::elem *logits,
-                                                          typename E::elem *out, FilterArgs a) {
+// ---------------------------------------------------------------------------
+// A row by any number of passes over memory: vocabularies of any size, values of any size.
+
+template <typename E, bool kVec, int NT>
+__device__ __forceinline__ void filter_any(const typename E::elem *logits, typename E::elem *out,
+                                           const FilterArgs &a, const FilterAsk &q, int64_t bt,
+                                           FilterLds<NT> &lds) {
   using elem = typename E::elem;
-  __shared__ FilterLds lds;
-  const int64_t b = blockIdx.x / a.T;
-  const int t = (int)(blockIdx.x % a.T);
-  const FilterAsk q = filter_ask(a, b);
-  if (!q.bad && a.n_rows && t >= a.n_rows[b]) return;
-  const int64_t off = (int64_t)blockIdx.x * a.V;
-  FilterRow<E, kVec> r{logits + off, a, lds, 0.0f, 0.0, 0.0};
+  const int64_t off = bt * a.V;
+  FilterRow<E, kVec, NT> r{logits + off, a, lds, 0.0f, 0.0, 0.0};
   Kept kept;
   const bool ok = !q.bad && filter_row<E, kVec>(r, q, kept);
-  const elem none = sizeof(elem) == 2 ? (elem)0xff80 : (elem)kNegInf;
   elem *const to = out + off;
-  if (!ok) {  // every row of the prefix is NaN
-    elem nan;
-    if constexpr (sizeof(elem) == 2) nan = 0x7fc0;
-    else nan = __uint_as_float(0x7fc00000u);
-    for (int64_t i = threadIdx.x; i < a.V; i += kFilterBlock) to[i] = nan;
-    return;
-  }
+  if (!ok) return fill_nan<E>(to, a.V);
+  const elem none = sizeof(elem) == 2 ? (elem)0xff80 : (elem)kNegInf;
   if constexpr (kVec) {
     constexpr int P = E::kPerVec;
-    for (int64_t i = (int64_t)threadIdx.x * P; i < a.V; i += (int64_t)kFilterBlock * P) {
+    for (int64_t i = (int64_t)threadIdx.x * P; i < a.V; i += (int64_t)NT * P) {
       const vec16 w = *reinterpret_cast<const vec16 *>(r.row + i);
       float x[P];
       E::unpack(w, x);
@@ -375,20 +395,15 @@ __global__ __launch_bounds__(kFilterBlock) void kr_filter(const typename E::elem
       *reinterpret_cast<vec16 *>(to + i) = v;
     }
   } else {
-    for (int64_t i = threadIdx.x; i < a.V; i += kFilterBlock)
+    for (int64_t i = threadIdx.x; i < a.V; i += NT)
       to[i] = kept.has(logit_key(E::at(r.row, i)), i) ? r.row[i] : none;
   }
 }
 
-template <typename E, bool kVec>
-__global__ __launch_bounds__(kFilterBlock) void kr_sample(const typename E::elem *logits,
-                                                          FilterArgs a) {
-  __shared__ FilterLds lds;
-  const int64_t b = blockIdx.x / a.T;
-  const int t = (int)(blockIdx.x % a.T);
-  const FilterAsk q = filter_ask(a, b);
-  if (!q.bad && a.n_rows && t >= a.n_rows[b]) return;
-  FilterRow<E, kVec> r{logits + (int64_t)blockIdx.x * a.V, a, lds, 0.0f, 0.0, 0.0};
+template <typename E, bool kVec, int NT>
+__device__ __forceinline__ void sample_any(const typename E::elem *logits, const FilterArgs &a,
+                                           const FilterAsk &q, int64_t b, int t, FilterLds<NT> &lds) {
+  FilterRow<E, kVec, NT> r{logits + (b * a.T + t) * a.V, a, lds, 0.0f, 0.0, 0.0};
   Kept kept;
   const bool ok = !q.bad && filter_row<E, kVec>(r, q, kept);
   auto weigh = [&](int64_t i, float z) -> unsigned long long {
@@ -397,28 +412,37 @@ __global__ __launch_bounds__(kFilterBlock) void kr_sample(const typename E::elem
   unsigned long long total = 0;
   if (ok) {
     r.slab_sums(weigh);
-    filter_scan(lds.slabs[threadIdx.x], total, lds);
+    block_scan<NT>(lds.slabs[threadIdx.x], total, lds.wave);
   }
   for (int k = 0; k < a.K; ++k) {
-    const int64_t at = (b * a.K + k) * a.T + t;
-    const double u = a.u ? a.u[at]
-                         : counter_uniform(a.seed, a.row_base + (uint64_t)b,
-                                           (uint64_t)k * (uint64_t)a.T + (uint64_t)t, kSample);
-    int32_t token = -1;
-    float lp = __uint_as_float(0x7fc00000u);
-    if (ok && u >= 0.0 && u < 1.0) {
-      unsigned long long x = (unsigned long long)(u * (double)total);
-      x = x < total ? x : total - 1;
-      const int64_t v = r.locate(x + 1, weigh);
-      token = (int32_t)v;
-      const double z = (double)E::at(r.row, v) - (double)r.m;
-      lp = (float)(z / (double)q.t - log(ldexp((double)total, -a.shift)));
-    }
-    if (threadIdx.x == 0) {
-      a.token[at] = token;
-      if (a.logprob) a.logprob[at] = lp;
-    }
+    const double u = draw_uniform(a, b, k, t);
+    int64_t v = -1;
+    if (ok && u >= 0.0 && u < 1.0) v = r.locate(draw_target(u, total), weigh);
+    if (threadIdx.x == 0)
+      put_draw(a, b, k, t, v, v < 0 ? 0.0f : E::at(r.row, v), r.m, q.t, total);
   }
+}
+
+template <typename E, bool kVec, int NT>
+__global__ __launch_bounds__(NT) void kr_filter_any(const typename E::elem *logits,
+                                                              typename E::elem *out,
+                                                              FilterArgs a) {
+  __shared__ FilterLds<NT> lds;
+  const int64_t b = blockIdx.x / a.T;
+  const FilterAsk q = filter_ask(a, b);
+  if (!q.bad && a.n_rows && (int)(blockIdx.x % a.T) >= a.n_rows[b]) return;
+  filter_any<E, kVec, NT>(logits, out, a, q, blockIdx.x, lds);
+}
+
+template <typename E, bool kVec, int NT>
+__global__ __launch_bounds__(NT) void kr_sample_any(const typename E::elem *logits,
+                                                              FilterArgs a) {
+  __shared__ FilterLds<NT> lds;
+  const int64_t b = blockIdx.x / a.T;
+  const int t = (int)(blockIdx.x % a.T);
+  const FilterAsk q = filter_ask(a, b);
+  if (!q.bad && a.n_rows && t >= a.n_rows[b]) return;
+  sample_any<E, kVec, NT>(logits, a, q, b, t, lds);
 }
 
 }  // namespace svd

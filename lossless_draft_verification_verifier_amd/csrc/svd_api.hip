@@ -20,6 +20,7 @@
 #include "kr_cps.hpp"
 #include "kr_draw.hpp"
 #include "kr_filter.hpp"
+#include "kr_filter_row.hpp"
 #include "kr_pages.hpp"
 #include "kr_rows.hpp"
 #include "kr_rowstats.hpp"

@@ -60,30 +60,69 @@ int filter_args(FilterArgs &a, svd_dtype_t dtype, int64_t B, int32_t T, int32_t 
   a.V = V;
   a.T = T;
   constexpr int64_t step = 8 * kFilterBlock;
-  a.slab = step * (((int64_t)V + step * kFilterSlabs - 1) / (step * kFilterSlabs));
+  a.slab = step * (((int64_t)V + step * kFilterBlock - 1) / (step * kFilterBlock));
   int bits = 0;  // V * 2^shift stays below 2^62
   while (((int64_t)1 << bits) < V) ++bits;
   a.shift = std::min(62 - bits, 50);
   return SVD_OK;
 }
 
-template <typename E, bool kVec>
-int filter_launch(const void *logits, void *out, const FilterArgs &a, int64_t rows,
-                  hipStream_t s) {
+// A row in one workgroup's registers, or in as many passes over memory as there are
+// searches (kr_filter_row.hpp), or by the passes that take any row (kr_filter.hpp): for
+// vocabularies that are past a row's records, and for small ones, where four workgroups
+// share a CU.
+constexpr int64_t kFilterSmall = 8192;
+
+template <typename E, int NV>
+int filter_held(const void *logits, void *out, const FilterArgs &a, int64_t rows, hipStream_t s) {
   using T_ = typename E::elem;
   CallTimer tm;
-  SVD_LAUNCH(tm, SVD_KERNEL_FILTER, s, kr_filter<E, kVec>, dim3((unsigned)rows),
-             dim3(kFilterBlock), s, static_cast<const T_ *>(logits), static_cast<T_ *>(out), a);
+  if (out) {
+    SVD_LAUNCH(tm, SVD_KERNEL_FILTER, s, kr_filter<E, kFilterBlock, NV>, dim3((unsigned)rows),
+               dim3(kFilterBlock), s, static_cast<const T_ *>(logits), static_cast<T_ *>(out), a);
+  } else {
+    SVD_LAUNCH(tm, SVD_KERNEL_SAMPLE, s, kr_sample<E, kFilterBlock, NV>, dim3((unsigned)rows),
+               dim3(kFilterBlock), s, static_cast<const T_ *>(logits), a);
+  }
   return SVD_OK;
 }
 
-template <typename E, bool kVec>
-int sample_launch(const void *logits, const FilterArgs &a, int64_t rows, hipStream_t s) {
+template <typename E, bool kVec, int NT>
+int filter_passes(const void *logits, void *out, const FilterArgs &a, int64_t rows,
+                  hipStream_t s) {
   using T_ = typename E::elem;
   CallTimer tm;
-  SVD_LAUNCH(tm, SVD_KERNEL_SAMPLE, s, kr_sample<E, kVec>, dim3((unsigned)rows),
-             dim3(kFilterBlock), s, static_cast<const T_ *>(logits), a);
+  if (out) {
+    SVD_LAUNCH(tm, SVD_KERNEL_FILTER, s, kr_filter_any<E, kVec, NT>, dim3((unsigned)rows), dim3(NT),
+               s, static_cast<const T_ *>(logits), static_cast<T_ *>(out), a);
+  } else {
+    SVD_LAUNCH(tm, SVD_KERNEL_SAMPLE, s, kr_sample_any<E, kVec, NT>, dim3((unsigned)rows), dim3(NT),
+               s, static_cast<const T_ *>(logits), a);
+  }
   return SVD_OK;
+}
+
+// out: nullptr for a sample call.
+template <typename E>
+int filter_rows(const void *logits, void *out, const FilterArgs &a, int64_t rows, hipStream_t s) {
+  constexpr int64_t es = sizeof(typename E::elem), P = E::kPerVec, step = P * kFilterBlock;
+  const bool alike = !out || ((uintptr_t)logits - (uintptr_t)out) % 16 == 0;
+  const int64_t most = a.V + P - 1;  // tokens of whole 16-byte pieces
+  if (alike && a.V > kFilterSmall) {
+    if (es == 2) {
+      if (most <= 5 * step) return filter_held<BF16, 5>(logits, out, a, rows, s);
+      if (most <= 10 * step) return filter_held<BF16, 10>(logits, out, a, rows, s);
+      if (most <= 19 * step) return filter_held<BF16, 19>(logits, out, a, rows, s);
+    }
+    if (most <= 64 * step) return filter_held<E, 0>(logits, out, a, rows, s);
+  }
+  const bool vec = a.V * es % 16 == 0 && ((uintptr_t)logits) % 16 == 0 &&
+                   ((uintptr_t)out) % 16 == 0;
+  if (a.V <= kFilterSmall)
+    return vec ? filter_passes<E, true, 256>(logits, out, a, rows, s)
+               : filter_passes<E, false, 256>(logits, out, a, rows, s);
+  return vec ? filter_passes<E, true, kFilterBlock>(logits, out, a, rows, s)
+             : filter_passes<E, false, kFilterBlock>(logits, out, a, rows, s);
 }
 
 // How the rows of the groups are cut: m_rows of one group, query heads of a kv head
@@ -267,14 +306,9 @@ int svd_filter_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
   if (((uintptr_t)out) % es != 0) return SVD_EINVAL;
   const uint64_t bytes = (uint64_t)(B * T) * (uint64_t)V * es;
   if (out != logits && overlap(out, bytes, logits, bytes)) return SVD_EINVAL;
-  const bool vec = ((size_t)V * es) % 16 == 0 && ((uintptr_t)logits) % 16 == 0 &&
-                   ((uintptr_t)out) % 16 == 0;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (dtype == SVD_BF16)
-    return vec ? filter_launch<BF16, true>(logits, out, a, B * T, s)
-               : filter_launch<BF16, false>(logits, out, a, B * T, s);
-  return vec ? filter_launch<F32, true>(logits, out, a, B * T, s)
-             : filter_launch<F32, false>(logits, out, a, B * T, s);
+  return dtype == SVD_BF16 ? filter_rows<BF16>(logits, out, a, B * T, s)
+                           : filter_rows<F32>(logits, out, a, B * T, s);
 }
 
 int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int32_t V, int32_t K,
@@ -292,14 +326,9 @@ int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int3
   a.row_base = row_base;
   a.token = token;
   a.logprob = logprob;
-  const bool vec =
-      ((size_t)V * (dtype == SVD_F32 ? 4 : 2)) % 16 == 0 && ((uintptr_t)logits) % 16 == 0;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (dtype == SVD_BF16)
-    return vec ? sample_launch<BF16, true>(logits, a, B * T, s)
-               : sample_launch<BF16, false>(logits, a, B * T, s);
-  return vec ? sample_launch<F32, true>(logits, a, B * T, s)
-             : sample_launch<F32, false>(logits, a, B * T, s);
+  return dtype == SVD_BF16 ? filter_rows<BF16>(logits, nullptr, a, B * T, s)
+                           : filter_rows<F32>(logits, nullptr, a, B * T, s);
 }
 
 size_t svd_prefix_attention_workspace_bytes(int64_t B, int32_t T, int32_t q_heads,
