@@ -29,6 +29,10 @@ constexpr int kSideBins = 35 << 7;           // counters of one sign
 constexpr int kBinLo = (127 - 26) << 7;      // the upper half of 2^-26
 constexpr int kRanks = 2 * kSideBins + 1;    // by falling value: positive, zero, negative
 constexpr float kBinTop = 512.0f;            // magnitudes below it have counters
+// Weights are found by a token's upper half with few steps: of each sign a slot for zero,
+// one per counter, and one, without weight, for what lies past them.
+constexpr int kSideSlots = kSideBins + 2;
+constexpr int kSlots = 2 * kSideSlots;
 constexpr int kRowEntries = 1024;            // (step, wave) records of a row at most
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -103,9 +107,9 @@ struct RowLds {
   // these the zeros' one
   static constexpr int kNeg = 32768;
   static constexpr int kWords = kNeg + kSideBins;
-  // in the gap between them: weights by rank, then the keys gathered around a cut
+  // in the gap between them: weights by slot, then the keys gathered around a cut
   static constexpr int kMassAt = kSideBins;
-  static constexpr int kListAt = kMassAt + 2 * kRanks;
+  static constexpr int kListAt = kMassAt + 2 * kSlots;
   static constexpr int kListCap = kNeg - 1 - kListAt;
   static_assert(kMassAt % 2 == 0 && kListCap >= 4096, "");
   uint32_t h[kWords];
@@ -131,12 +135,11 @@ __device__ __forceinline__ int rank_word(int r) {
   return r < kSideBins ? kSideBins - 1 - r : RowLds<1024>::kNeg - 1 + (r - kSideBins);
 }
 __device__ __forceinline__ float rank_value(int r) { return __uint_as_float(rank_bits(r) << 16); }
-// (of bits that have a counter, or of a zero)
-__device__ __forceinline__ int bits_rank(uint32_t u) {
-  const uint32_t a = u & 0x7fffu;
-  if (a == 0) return kSideBins;
-  return u >> 15 ? (int)(a - kBinLo) + kSideBins + 1 : (int)(kBinLo + kSideBins - 1 - a);
+__device__ __forceinline__ int bits_slot(uint32_t u) {
+  const int a = (int)(u & 0x7fffu) - kBinLo;
+  return (int)(u >> 15) * kSideSlots + 1 + min(max(a, -1), kSideBins);
 }
+__device__ __forceinline__ int rank_slot(int r) { return bits_slot(rank_bits(r)); }
 
 template <typename E, int NT, int NV>
 struct HeldRow {
@@ -443,23 +446,22 @@ struct HeldRow {
     if (threadIdx.x == 0) l.n_list = 0;
     lds_barrier();
     uint32_t *const list = l.list();
-    const int lane = threadIdx.x & 63;
     each([&](int j, const vec16 &v) {
       uint32_t in = 0;
       tokens(v, [&](int e, uint32_t bits) {
         const bool hit = u ? bits >> 16 == u : (bits & 0x7fffffffu) == 0;
         in |= (uint32_t)hit << e;
       });
-      if (!__any(in)) return;
+      if (!in) return;
       tokens(v, [&](int e, uint32_t bits) {
         const float x = __uint_as_float(bits);
-        const bool hit = (in >> e & 1) && (x > zt || (x == zt && first(j) + e < tie));
-        const unsigned long long who = __ballot(hit);
-        if (who) {
-          int to = 0;
-          if (lane == 0) to = atomicAdd(&l.n_list, (int)__popcll(who));
-          to = __builtin_amdgcn_readfirstlane(to) + (int)__popcll(who & ((1ull << lane) - 1));
-          if (hit && to < Lds::kListCap) list[to] = logit_key(x);
+        if (!(x > zt || (x == zt && first(j) + e < tie))) in &= ~(1u << e);
+      });
+      int to = atomicAdd(&l.n_list, (int)__popc(in));
+      tokens(v, [&](int e, uint32_t bits) {
+        if (in >> e & 1) {
+          if (to < Lds::kListCap) list[to] = logit_key(__uint_as_float(bits));
+          ++to;
         }
       });
     });
@@ -608,9 +610,12 @@ __device__ __forceinline__ uint32_t held_cut(HeldRow<E, NT, NV> &r, const Filter
         const float z = rank_value(rank);
         if (z >= least) w = r.weight(z);
       }
-      mass[rank] = w;
+      mass[rank_slot(rank)] = w;
       mine += k * w;
     });
+    if (threadIdx.x < 2) mass[threadIdx.x * kSideSlots + kSideSlots - 1] = 0;
+    lds_barrier();
+    if (threadIdx.x == 0) mass[kSideSlots] = mass[0];  // -0.0
     if (!by_p) {
       lds_barrier();
       return 0;
@@ -619,10 +624,12 @@ __device__ __forceinline__ uint32_t held_cut(HeldRow<E, NT, NV> &r, const Filter
     r.cross(mine, [&](unsigned long long total) {
       target = (unsigned long long)ceil(fmax((double)q.p, 0.0) * (double)total);
       return target = target < 1 ? 1 : target > total ? total : target;
-    }, [&](int rank) { return mass[rank] * (rank == rank_k ? n_k : l.h[rank_word(rank)]); });
+    }, [&](int rank) {
+      return mass[rank_slot(rank)] * (rank == rank_k ? n_k : l.h[rank_word(rank)]);
+    });
     const int rank = l.rank;
     target -= l.found[0];  // of this rank
-    const unsigned long long w = mass[rank];
+    const unsigned long long w = mass[rank_slot(rank)];
     const uint32_t k = (uint32_t)((target + w - 1) / w);
     zt = rank_value(rank);
     if (k < l.h[rank_word(rank)]) tie = r.behind_tie(zt, k);
@@ -640,7 +647,7 @@ __device__ __forceinline__ uint32_t held_cut(HeldRow<E, NT, NV> &r, const Filter
     }
     if (!by_p) return 0;
     unsigned long long *const mass = l.mass();
-    for (int i = threadIdx.x; i < kRanks; i += NT) mass[i] = 0;
+    for (int i = threadIdx.x; i < kSlots; i += NT) mass[i] = 0;
     lds_barrier();
     r.each([&](int j, const vec16 &v) {
       const int i0 = r.first(j);
@@ -648,18 +655,20 @@ __device__ __forceinline__ uint32_t held_cut(HeldRow<E, NT, NV> &r, const Filter
         const float z = __uint_as_float(bits);
         if ((z > zt || (z == zt && i0 + e < tie)) && z > -kBinTop) {
           const unsigned long long w = r.weight(z);
-          if (w) atomicAdd(&mass[bits_rank(bits >> 16)], w);
+          if (w) atomicAdd(&mass[bits_slot(bits >> 16)], w);
         }
       });
     });
     lds_barrier();
     unsigned long long mine = 0;
-    Row::ranks([&](int, int rank) { mine += mass[rank]; });
+    if (threadIdx.x == 0) mass[0] += mass[kSideSlots];  // one rank for both zeros
+    lds_barrier();
+    Row::ranks([&](int, int rank) { mine += mass[rank_slot(rank)]; });
     unsigned long long target = 0;
     r.cross(mine, [&](unsigned long long total) {
       target = (unsigned long long)ceil(fmax((double)q.p, 0.0) * (double)total);
       return target = target < 1 ? 1 : target > total ? total : target;
-    }, [&](int rank) { return mass[rank]; });
+    }, [&](int rank) { return mass[rank_slot(rank)]; });
     const int rank = l.rank;
     target -= l.found[0];
     float z;
@@ -774,11 +783,21 @@ void kr_sample(const typename E::elem *logits, FilterArgs a) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   // the sums of the kept weights in every wave's piece; most pieces have none
   unsigned long long *const mass = l.mass();
+  if constexpr (Row::kShort) {  // ranks below the cut have none
+    Row::ranks([&](int, int rank) {
+      if (rank_value(rank) < zt) mass[rank_slot(rank)] = 0;
+    });
+    if (threadIdx.x == 0 && 0.0f < zt) mass[kSideSlots] = 0;
+    lds_barrier();
+  }
   auto weigh = [&](int i, uint32_t bits) -> unsigned long long {
     const float z = __uint_as_float(bits);
-    if (!(z > zt || (z == zt && i < tie)) || !(z > -kBinTop)) return 0;
-    if constexpr (Row::kShort) return mass[bits_rank(bits >> 16)];
-    else return r.weight(z);
+    if constexpr (Row::kShort) {
+      return z == zt && i >= tie ? 0ull : mass[bits_slot(bits >> 16)];
+    } else {
+      if (!(z > zt || (z == zt && i < tie)) || !(z > -kBinTop)) return 0;
+      return r.weight(z);
+    }
   };
   auto sum_of = [&](int i0, const vec16 &v) {
     unsigned long long s = 0;
