@@ -57,7 +57,8 @@ enum {
   SVD_KERNEL_FILTER = 24,       /* tokens that temperature, min-p, top-k and top-p keep   */
   SVD_KERNEL_SAMPLE = 25,       /* draws among the kept tokens                            */
   SVD_KERNEL_SHARE = 26,        /* tokens that the sequences of a group have in common    */
-  SVD_KERNEL_COUNT = 27
+  SVD_KERNEL_SHARED_ATTENTION = 27, /* a group's rows over the tokens that it shares      */
+  SVD_KERNEL_COUNT = 28
 };
 
 int svd_profile_enable(unsigned kernel_mask);

@@ -48,7 +48,8 @@ SVD_CACHE_BF16, SVD_CACHE_E4M3 = 0, 1
 KERNELS = ("rowstats", "select", "draw_pass", "draw_pick", "beta", "mark", "pool_stats",
            "alpha_rows", "lattice", "beam", "lattice_len", "combine", "rowstats_split",
            "rowstats_live", "adl", "beta_combine", "draft_tree", "cache_write", "cache_read",
-           "tree_attention", "attention_join", "adjust", "pages", "slots", "filter", "sample", "share")
+           "tree_attention", "attention_join", "adjust", "pages", "slots", "filter", "sample", "share",
+           "shared_attention")
 SVD_RULE_STANDARD, SVD_RULE_GREEDY = 0, 1
 
 C_EXPORTS = ("svd_workspace_bytes", "svd_verify", "svd_select_and_verify", "svd_greedy_verify",

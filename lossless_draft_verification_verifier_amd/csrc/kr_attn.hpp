@@ -65,13 +65,26 @@ constexpr int kAttnJoinBlock = 256;
 constexpr int kAttnMaxSplits = 64;
 
 // Sequences lo .. hi - 1 of a batch whose first `tokens` cached tokens are in the same pages,
-// those of sequence `first`.  tokens is a multiple of kShareTokens.
+// those of sequence `first`.  tokens is a multiple of kShareTokens.  Their rows are cut into
+// tiles of m_rows; a unit is a tile of one kv head, head by head, `steps` tiles of tokens
+// long, and the units of all groups, one behind the other, are one line of steps.
 constexpr int kShareTokens = 128;
 struct ShareGroup {
   int32_t lo, hi, first, tokens;
+  int32_t nodes;            // nodes in use of its sequences, listed from lo * T on
+  int32_t tiles, steps;     // row tiles; steps of a unit
+  int32_t unit0;            // its first unit, and where that begins on the line
+  int64_t step0;
 };
-struct ShareTile {          // rows of a group that one workgroup takes
-  int32_t group, row;       // group -1: none
+// Workgroup w takes steps w * per .. of the line, and leaves a part for each unit that it meets:
+// part unit + w, in m_rows rows.
+struct ShareCut {
+  int64_t total, per;
+};
+struct ShareSeq {           // one sequence
+  int32_t eff;              // tokens that the shared parts cover
+  int32_t group, start;     // its group, and its first node's number there
+  int32_t pad;
 };
 
 struct AttnArgs {
@@ -87,14 +100,17 @@ struct AttnArgs {
   float *part_o;            // [S][B][T][Hq][D] when S > 1
   float *part_ms;           // [S][B][T][Hq][2]
   int64_t rows_all;         // B * T * Hq
-  int parts, part0;         // parts of a row in all, and before this kernel's
   // scores that are capped or fall off with distance, and shared prefixes (kForm)
   float cap_in, cap_out;    // 2 log2(e) scale / cap and cap * log2(e); 0: no cap
   const float *slopes;      // [Hq] or null
   const int32_t *depth;     // [B][T] or null: a chain
-  const int32_t *eff;       // [B] tokens that the shared parts cover, or null
+  const ShareSeq *seqs;     // [B], or null: nothing is shared
   const ShareGroup *groups;
-  const ShareTile *tiles;
+  const ShareCut *cut;
+  const int32_t *nodes;     // [B][T] b * T + t of the groups' nodes
+  const float *share_o;     // [parts][share_rows][D]
+  const float *share_ms;    // [parts][share_rows][2]
+  int share_rows;
 };
 
 __device__ __forceinline__ f32x4 mfma_bf16(const vec16 &a, const vec16 &b, const f32x4 &c) {
@@ -163,6 +179,43 @@ __device__ __forceinline__ void attn_row_out(const AttnArgs &a, int64_t row, int
     a.lse[row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.6931471805599453f;
 }
 
+// The shared parts of row (node t of sequence b, query head i of kv head h): `at` rows into the
+// first of `n` parts.
+struct ShareRow {
+  int64_t at;
+  int n;
+};
+__device__ __forceinline__ ShareRow share_row(const AttnArgs &a, int64_t b, int t, int i, int h) {
+  const ShareSeq q = a.seqs[b];
+  if (q.eff == 0) return ShareRow{0, 0};
+  const ShareGroup g = a.groups[q.group];
+  const int64_t R = (int64_t)(q.start + t) * a.group + i;
+  const int64_t unit = (int64_t)h * g.tiles + R / a.share_rows;
+  const int64_t s0 = g.step0 + unit * g.steps, per = a.cut->per;
+  const int64_t w0 = s0 / per, w1 = (s0 + g.steps - 1) / per;
+  return ShareRow{(g.unit0 + unit + w0) * a.share_rows + R % a.share_rows, (int)(w1 - w0) + 1};
+}
+// 4 elements of a row's own part (exponent m, sum l) joined by those of its shared parts.
+template <int D>
+__device__ __forceinline__ void share_join(const AttnArgs &a, const ShareRow &r, int d, f32x4 &o,
+                                           float &m, float &l) {
+  float mm = m;
+  for (int s = 0; s < r.n; ++s)
+    mm = fmaxf(mm, a.share_ms[2 * (r.at + (int64_t)s * a.share_rows)]);
+  const float f = part_factor(m, l, mm);
+  o *= f;
+  l *= f;
+#pragma unroll 2
+  for (int s = 0; s < r.n; ++s) {
+    const int64_t at = r.at + (int64_t)s * a.share_rows;
+    const float ms = a.share_ms[2 * at], ls = a.share_ms[2 * at + 1];
+    const float g = part_factor(ms, ls, mm);
+    l += ls * g;
+    o += *reinterpret_cast<const f32x4 *>(a.share_o + at * D + d) * g;
+  }
+  m = mm;
+}
+
 // 32 bits of node t's ancestors from bit i0 on; bits below 0 are context, which
 // every row attends to.  words null: a chain.
 __device__ __forceinline__ uint32_t allow_window(const uint32_t *words, int W, int t, int i0) {
@@ -193,17 +246,15 @@ struct AttnShape {
   static constexpr int kLdsBytes = 2 * kTileBytes > kJoinBytes ? 2 * kTileBytes : kJoinBytes;
 };
 
-// What a kernel computes: a prefix's rows over all of its tokens; the same behind the
-// tokens that a group shares (none without groups), with shaped scores; or a group's rows,
-// of all of its sequences, over the tokens that they share.
-enum AttnForm { kTree = 0, kShaped = 1, kShared = 2, kSharedShaped = 3 };
+// What a kernel computes: a prefix's rows over all of its tokens; or the same behind the
+// tokens that its group shares (none without groups), with shaped scores where asked.
+enum AttnForm { kTree = 0, kShaped = 1 };
 
 template <int D, bool kE4M3, int NT, int WQ, int WT, int kForm>
 __global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
                              (AttnShape<D, kE4M3, NT, WQ, WT>::kMinWaves))
 void kr_tree_attention(CacheView cv, AttnArgs a) {
-  constexpr bool kRows = kForm == kShared || kForm == kSharedShaped;
-  constexpr bool kShape = kForm == kShaped || kForm == kSharedShaped;
+  constexpr bool kShape = kForm == kShaped;
   using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
   constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
   constexpr bool kRoles = Shape::kRoles;
@@ -224,44 +275,19 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // units on neighbouring blocks run on different XCDs; the row tiles of one
   // unit, which read the same keys and values, stay on one
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  int unit = (idx / a.m_tiles) * 8 + xcd, mt = idx % a.m_tiles;
-  if (kRows && (a.units & 7)) {  // few units of many rows: on all XCDs, wherever they read
-    unit = blockIdx.x % a.units;
-    mt = blockIdx.x / a.units;
-    if (mt >= a.m_tiles) return;
-  }
+  const int unit = (idx / a.m_tiles) * 8 + xcd, mt = idx % a.m_tiles;
   if (unit >= a.units) return;
   const int s = unit % a.S, bh = unit / a.S;
   const int h = bh % cv.Hkv;
+  const int64_t b = bh / cv.Hkv;
   const int Hq = cv.Hkv * a.group;
-  int64_t b = bh / cv.Hkv;  // whose pages are read
-  int ctx, nodes, rows, r_lo, b_lo = 0;
-  bool bad = false;
-  if constexpr (kRows) {
-    const ShareTile st = a.tiles[mt];
-    if (st.group < 0) return;
-    const ShareGroup sg = a.groups[st.group];
-    if (sg.tokens == 0) return;
-    b = sg.first;
-    b_lo = sg.lo;
-    ctx = sg.tokens;
-    nodes = 0;
-    rows = (sg.hi - sg.lo) * a.T * a.group;
-    r_lo = st.row;
-  } else {
-    ctx = a.ctx_len[b];
-    nodes = a.n_nodes ? a.n_nodes[b] : a.T;
-    // lengths out of range: every row of the prefix is NaN
-    bad = attn_bad(ctx, nodes, a.T, a.room);
-    rows = (bad ? a.T : nodes) * a.group;
-    r_lo = mt * a.m_rows;
-  }
-  const int r_hi = min(r_lo + a.m_rows, rows);  // this workgroup's rows
+  const int ctx = a.ctx_len[b];
+  const int nodes = a.n_nodes ? a.n_nodes[b] : a.T;
+  // lengths out of range: every row of the prefix is NaN
+  const bool bad = attn_bad(ctx, nodes, a.T, a.room);
+  const int rows = (bad ? a.T : nodes) * a.group;
+  const int r_lo = mt * a.m_rows, r_hi = min(r_lo + a.m_rows, rows);  // this workgroup's rows
   if (r_lo >= r_hi) return;
-  // a row's token among the batch's B * T, its node and its query head in the group
-  auto token_of = [&](int R) -> int64_t {
-    return kRows ? (int64_t)b_lo * a.T + R / a.group : b * a.T + R / a.group;
-  };
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int W = (a.T + 31) / 32;
@@ -269,11 +295,15 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   const int total = bad ? 0 : ctx + nodes;
   // a sequence's room goes up to 2^31 - page: sums past its length are 64 bits
   const int all_tiles = (int)(((int64_t)total + TK - 1) / TK);
-  const int first = kForm == kShaped && a.eff && !bad ? a.eff[b] / TK : 0;
+  const int first = kShape && a.seqs && !bad ? a.seqs[b].eff / TK : 0;
   const int per = (all_tiles - first + a.S - 1) / a.S;
   const int t_lo = first + s * per, t_hi = min(t_lo + per, all_tiles);
 
+  __shared__ ShareRow lds_share[kShape ? M : 1];
   if (threadIdx.x == 0) lds_odd = 0;
+  if (kShape && first && a.S == 1)
+    for (int r = r_lo + (int)threadIdx.x; r < r_hi; r += Shape::kBlock)
+      lds_share[r - r_lo] = share_row(a, b, r / a.group, r % a.group, h);
   __syncthreads();
 
   // the threads that bring a tile to LDS: the loading waves do keys and values,
@@ -354,7 +384,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // registers to LDS.  A token without a valid page gets NaN keys, so that every row
   // that attends to it is NaN; values behind the end are zero.
   auto store_tile = [&](const Staged &st, int tile) {
-    const bool last = !kRows && (int64_t)tile * TK + TK > ctx;  // holds nodes or the end
+    const bool last = (int64_t)tile * TK + TK > ctx;  // holds nodes or the end
     vec16 *const lk = reinterpret_cast<vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
     const int left = min((int64_t)TK, total - (int64_t)tile * TK);
@@ -448,15 +478,14 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = min(r_lo + (wq * NT + t) * 16 + n, r_hi - 1);
-    const int64_t token = token_of(r);
     node[t] = r / a.group;
-    const uint16_t *q = a.q + token * a.q_stride + (int64_t)(h * a.group + r % a.group) * D;
+    const uint16_t *q = a.q + (b * a.T + node[t]) * a.q_stride +
+                        (int64_t)(h * a.group + r % a.group) * D;
     if constexpr (kShape) {
       pos[t] = 0;
       slope[t] = 0.0f;
       if (a.slopes) {
-        const int64_t rb = token / a.T;
-        pos[t] = a.ctx_len[rb] + (a.depth ? a.depth[token] : (int)(token % a.T));
+        pos[t] = ctx + (a.depth ? a.depth[b * a.T + node[t]] : node[t]);
         slope[t] = a.slopes[h * a.group + r % a.group] * 1.4426950408889634f;
       }
     }
@@ -479,7 +508,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   if (t_lo < t_hi) before();
   for (int tile = t_lo; tile < t_lo + steps; ++tile) {
     const int64_t p0 = (int64_t)tile * TK;
-    const bool last = !kRows && p0 + TK > ctx;  // holds nodes or the end
+    const bool last = p0 + TK > ctx;  // holds nodes or the end
     const vec16 *const lk =
         reinterpret_cast<const vec16 *>(lds + ((tile - t_lo) & 1) * Shape::kTileBytes);
     const unsigned char *const lv = lds + ((tile - t_lo) & 1) * Shape::kTileBytes + TK * D * 2;
@@ -680,17 +709,19 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   __syncthreads();  // the parts of all waves are there
 
   // one row's 4 elements from d on, its exponent and its sum
-  auto put = [&](int R, int d, f32x4 x, float mm, float ll, bool first) {
-    const int64_t row = token_of(R) * Hq + h * a.group + R % a.group;
-    if (a.parts > 1) {
-      const int64_t pr = (int64_t)(a.part0 + s) * a.rows_all + row;
+  auto put = [&](int R, int d, f32x4 x, float mm, float ll) {
+    const int64_t row = (b * a.T + R / a.group) * Hq + h * a.group + R % a.group;
+    if (a.S > 1) {
+      const int64_t pr = (int64_t)s * a.rows_all + row;
       *reinterpret_cast<f32x4 *>(a.part_o + pr * D + d) = x;
-      if (first) {
+      if (d == 0) {
         a.part_ms[2 * pr] = mm;
         a.part_ms[2 * pr + 1] = ll;
       }
     } else {
-      attn_row_out<D>(a, row, d, x, mm, ll, first);
+      // shared parts are there already: the row ends here
+      if (kShape && first) share_join<D>(a, lds_share[R - r_lo], d, x, mm, ll);
+      attn_row_out<D>(a, row, d, x, mm, ll, d == 0);
     }
   };
   // what the tokens of this part whose values are not finite add to 4 elements
@@ -756,9 +787,8 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       ll += lds_ms[w][r][1] * f;
       x += *reinterpret_cast<const f32x4 *>(&lo[w][r][d]) * f;
     }
-    if constexpr (!kRows)
-      if (lds_odd) x = odd_values(r_lo + r, d, x, mm);
-    put(r_lo + r, d, x, mm, ll, d == 0);
+    if (lds_odd) x = odd_values(r_lo + r, d, x, mm);
+    put(r_lo + r, d, x, mm, ll);
   }
 }
 
@@ -774,20 +804,23 @@ __global__ __launch_bounds__(kAttnJoinBlock) void kr_attn_join(AttnArgs a, int H
   const int nodes = a.n_nodes ? a.n_nodes[b] : a.T;
   // a prefix out of range wrote NaN parts for every row
   if (bt % a.T >= nodes && !attn_bad(a.ctx_len[b], nodes, a.T, a.room)) return;
-  // a sequence that shares nothing has no shared parts
-  const int s0 = a.eff && a.eff[b] == 0 ? a.part0 : 0;
   float m = kNegInf;
 #pragma unroll 8
-  for (int s = s0; s < a.parts; ++s) m = fmaxf(m, a.part_ms[2 * (s * a.rows_all + row)]);
+  for (int s = 0; s < a.S; ++s) m = fmaxf(m, a.part_ms[2 * (s * a.rows_all + row)]);
   float l = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-  for (int s = s0; s < a.parts; ++s) {
+  for (int s = 0; s < a.S; ++s) {
     const int64_t pr = s * a.rows_all + row;
     const float ms = a.part_ms[2 * pr], ls = a.part_ms[2 * pr + 1];
     const float f = part_factor(ms, ls, m);
     l += ls * f;
     o += *reinterpret_cast<const f32x4 *>(a.part_o + pr * D + d) * f;
+  }
+  if (a.seqs) {
+    const int h = (int)(row % Hq);
+    const ShareRow r = share_row(a, b, (int)(bt % a.T), h % a.group, h / a.group);
+    if (r.n) share_join<D>(a, r, d, o, m, l);
   }
   attn_row_out<D>(a, row, d, o, m, l, d == 0);
 }

@@ -9,24 +9,34 @@
 #pragma once
 
 #include "kr_attn.hpp"
+#include "kr_pages.hpp"
 
 namespace svd {
 
 constexpr int kShareBlock = 1024;
+constexpr int kShareWorkgroups = 256;  // of the attention: one per CU
+constexpr int kShareMinSteps = 2;      // a workgroup takes at least as many, where there are
 
 struct ShareArgs {
   const int32_t *off;       // [G + 1]
   const int32_t *ctx_len, *n_nodes, *table;
   int64_t B, G, room;
-  int T, max_pages, page_shift, group, m_rows, m_tiles;
-  int32_t *eff;             // [B]
+  int T, max_pages, page_shift, group, heads, m_rows, tile;
+  ShareSeq *seqs;           // [B]
+  int32_t *nodes;           // [B][T]
   ShareGroup *groups;       // [G]
-  ShareTile *tiles;         // [m_tiles]
+  ShareCut *cut;
 };
+
+__device__ __forceinline__ void share_cut(ShareCut *cut, int64_t total) {
+  cut->total = total;
+  cut->per = max((total + kShareWorkgroups - 1) / kShareWorkgroups, (int64_t)kShareMinSteps);
+}
 
 __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
   __shared__ int lo_ok, n_act, first, ctx_min, pages;
   __shared__ int wave_sum[kShareBlock / 64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t g = blockIdx.x;
   if (threadIdx.x == 0) {
     lo_ok = 1;
@@ -60,36 +70,27 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
   if (threadIdx.x == 0) pages = cols;
   __syncthreads();
   if (cols > 0) {
-    // entries of all tables, a run of columns per sequence
-    const int64_t n = (int64_t)(hi - lo) * cols;
-    int least = cols;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += kShareBlock) {
-      const int b = lo + (int)(i / cols), c = (int)(i % cols);
-      const bool same = a.table[(int64_t)b * a.max_pages + c] == a.table[(int64_t)f * a.max_pages + c];
-      if (!same && c < least && active(b)) least = c;
+    // a wave per sequence, four columns of a lane at a time
+    const int32_t *const one = a.table + (int64_t)f * a.max_pages;
+    for (int b = lo + w; b < hi; b += kShareBlock / 64) {
+      if (b == f || !active(b)) continue;
+      const int32_t *const other = a.table + (int64_t)b * a.max_pages;
+      for (int c0 = 0; c0 < pages; c0 += 256) {  // (pages only falls)
+        int least = cols;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          const int c = c0 + 64 * i + lane, at = min(c, cols - 1);
+          if (one[at] != other[at]) least = at;
+        }
+        if (least < cols) atomicMin(&pages, least);
+        if (__any(least < cols)) break;
+      }
     }
-    if (least < cols) atomicMin(&pages, least);
   }
   __syncthreads();
   const int tokens = (int)(((int64_t)pages << a.page_shift) / kShareTokens * kShareTokens);
-  if (threadIdx.x == 0) a.groups[g] = ShareGroup{lo, hi, f, tokens};
-  for (int b = lo + (int)threadIdx.x; b < hi; b += kShareBlock)
-    a.eff[b] = tokens && active(b) ? tokens : 0;
-  // sequences of no group
-  const int64_t in_lo = valid ? a.off[0] : 0, in_hi = valid ? a.off[a.G] : 0;
-  for (int64_t b = g + (int64_t)threadIdx.x * a.G; b < a.B; b += (int64_t)kShareBlock * a.G)
-    if (b < in_lo || b >= in_hi) a.eff[b] = 0;
-  if (g != 0) return;
-  // the workgroups' rows: m_rows of a group each
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int before = 0;
-  for (int64_t i0 = 0; i0 < a.G; i0 += kShareBlock) {
-    const int64_t i = i0 + threadIdx.x;
-    int n = 0;
-    if (i < a.G && valid)
-      n = (int)(((int64_t)(a.off[i + 1] - a.off[i]) * a.T * a.group + a.m_rows - 1) / a.m_rows);
-    int up = n;
+  // inclusive sums over the workgroup, and the total
+  auto scan = [&](int up, int &total) {
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int x = __shfl_up(up, off, 64);
@@ -97,20 +98,75 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
     }
     if (lane == 63) wave_sum[w] = up;
     __syncthreads();
-    int total = 0;
+    total = 0;
     for (int k = 0; k < kShareBlock / 64; ++k) {
       if (k == w) up += total;
       total += wave_sum[k];
     }
-    for (int k = 0; k < n; ++k) {
-      const int at = before + up - n + k;
-      if (at < a.m_tiles) a.tiles[at] = ShareTile{(int32_t)i, k * a.m_rows};
-    }
-    before += total;
     __syncthreads();
+    return up;
+  };
+  // the nodes in use, one after another: rows that no node has are no workgroup's
+  int listed = 0;
+  for (int b0 = lo; b0 < hi; b0 += kShareBlock) {
+    const int b = b0 + (int)threadIdx.x;
+    int n = 0, total;
+    if (b < hi) {
+      n = tokens && active(b) ? (a.n_nodes ? a.n_nodes[b] : a.T) : 0;
+    }
+    const int from = listed + scan(n, total) - n;
+    listed += total;
+    if (b < hi) a.seqs[b] = ShareSeq{n ? tokens : 0, (int32_t)g, from, 0};
+    // a wave's sequences, one after another
+    for (unsigned long long who = __ballot(n > 0); who; who &= who - 1) {
+      const int k = __builtin_ctzll(who);
+      const int kn = __builtin_amdgcn_readlane(n, k), kf = __builtin_amdgcn_readlane(from, k);
+      const int64_t kb = (int64_t)b0 + w * 64 + k;
+      for (int t = lane; t < kn; t += 64)
+        a.nodes[(int64_t)lo * a.T + kf + t] = (int32_t)(kb * a.T + t);
+    }
   }
-  for (int i = before + (int)threadIdx.x; i < a.m_tiles; i += kShareBlock)
-    a.tiles[i] = ShareTile{-1, 0};
+  // sequences of no group
+  const int64_t in_lo = valid ? a.off[0] : 0, in_hi = valid ? a.off[a.G] : 0;
+  for (int64_t b = g + (int64_t)threadIdx.x * a.G; b < a.B; b += (int64_t)kShareBlock * a.G)
+    if (b < in_lo || b >= in_hi) a.seqs[b] = ShareSeq{0, 0, 0, 0};
+  if (threadIdx.x != 0) return;
+  ShareGroup s;
+  s.lo = lo;
+  s.hi = hi;
+  s.first = f;
+  s.tokens = listed ? tokens : 0;
+  s.nodes = listed;
+  s.tiles = (int)(((int64_t)listed * a.group + a.m_rows - 1) / a.m_rows);
+  s.steps = s.tokens / a.tile;
+  s.unit0 = 0;
+  s.step0 = 0;
+  a.groups[g] = s;
+  if (a.G == 1) share_cut(a.cut, (int64_t)s.tiles * a.heads * s.steps);
+}
+
+// The groups' places on the line, where there are several.
+__global__ __launch_bounds__(kShareBlock) void kr_share_cut(ShareArgs a) {
+  __shared__ int64_t lds[kShareBlock / 64][2];
+  int64_t units = 0, steps = 0;  // before this chunk of groups
+  for (int64_t i0 = 0; i0 < a.G; i0 += kShareBlock) {
+    const int64_t i = i0 + threadIdx.x;
+    int64_t u = 0, s = 0;
+    if (i < a.G) {
+      const ShareGroup g = a.groups[i];
+      u = g.tokens ? (int64_t)g.tiles * a.heads : 0;
+      s = u * g.steps;
+    }
+    int64_t upu = u, ups = s, tu, ts;
+    block_scan2<kShareBlock>(upu, ups, tu, ts, lds);
+    if (i < a.G) {
+      a.groups[i].unit0 = (int32_t)(units + upu - u);
+      a.groups[i].step0 = steps + ups - s;
+    }
+    units += tu;
+    steps += ts;
+  }
+  if (threadIdx.x == 0) share_cut(a.cut, steps);
 }
 
 }  // namespace svd

@@ -26,6 +26,7 @@
 #include "kr_rowstats.hpp"
 #include "kr_select.hpp"
 #include "kr_share.hpp"
+#include "kr_shared.hpp"
 #include "kr_tree.hpp"
 
 namespace {

@@ -125,37 +125,44 @@ int filter_rows(const void *logits, void *out, const FilterArgs &a, int64_t rows
              : filter_passes<E, false, kFilterBlock>(logits, out, a, rows, s);
 }
 
-// How the rows of the groups are cut: m_rows of one group, query heads of a kv head
-// included, per workgroup, and the shared tokens into S parts.
-AttnPlan share_plan(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t room,
-                    int64_t G) {
-  AttnPlan p;
-  const int64_t rows = B * T * (Hq / Hkv);
-  p.nt = rows <= 64 ? 1 : 2;
-  p.wq = rows <= 16 ? 1 : rows <= 64 ? 4 : 8;
-  p.wt = rows <= 16 ? 2 : 1;
-  p.m_rows = 16 * p.nt * p.wq;
-  p.m_tiles = (int)(rows / p.m_rows + G);
-  // The parts' time by a model of its two costs: rounds of workgroups, one per CU (two of the
-  // small ones), of tiles at 2.5 us each, and every part of a row written and read back.
-  const int64_t tk = 8192 / D, tiles = std::max<int64_t>(1, room / tk);
-  const int64_t base = (int64_t)p.m_tiles * Hkv, at_once = p.nt == 1 ? 2 * kAttnCus : kAttnCus;
-  const double part = (double)(B * T) * Hq * D * 8.0 / 4.0e6;
-  double best = 0.0;
-  p.S = 1;
-  for (int64_t S = 1; S <= std::min<int64_t>(kAttnMaxSplits, std::max<int64_t>(1, tiles / 2)); ++S) {
-    const double us = (double)((base * S + at_once - 1) / at_once) * ((tiles + S - 1) / S) * 2.5 +
-                      (double)S * part;
-    if (S == 1 || us < best) {
-      best = us;
-      p.S = (int)S;
-    }
+// Rows of a workgroup of the shared part: 256, or 64 with the tokens split over its waves
+// where there are no more.
+int share_rows(int64_t B, int32_t T, int64_t group) {
+  return B * T * group <= 64 ? SharedShape<128, 1, 2>::M : SharedShape<128, 2, 1>::M;
+}
+
+template <int D, bool kE4M3, int RB, int WT>
+int shared_launch(const CacheView &c, const AttnArgs &a, int64_t G, float *o, float *ms,
+                  hipStream_t s) {
+  CallTimer tm;
+  if (a.cap_in > 0.0f || a.slopes) {
+    SVD_LAUNCH(tm, SVD_KERNEL_SHARED_ATTENTION, s, kr_shared_attention<D, kE4M3, RB, WT, true>,
+               dim3(kShareWorkgroups), dim3(kSharedBlock), s, c, a, G, o, ms);
+  } else {
+    SVD_LAUNCH(tm, SVD_KERNEL_SHARED_ATTENTION, s, kr_shared_attention<D, kE4M3, RB, WT, false>,
+               dim3(kShareWorkgroups), dim3(kSharedBlock), s, c, a, G, o, ms);
   }
-  return p;
+  return SVD_OK;
+}
+
+template <int D, bool kE4M3>
+int shared_rows(const CacheView &c, const AttnArgs &a, int64_t G, float *o, float *ms,
+                hipStream_t s) {
+  return a.share_rows == 64 ? shared_launch<D, kE4M3, 1, 2>(c, a, G, o, ms, s)
+                            : shared_launch<D, kE4M3, 2, 1>(c, a, G, o, ms, s);
+}
+
+int shared_kind(const svd_cache_t *cache, const CacheView &c, const AttnArgs &a, int64_t G,
+                float *o, float *ms, hipStream_t s) {
+  if (cache->dtype == SVD_CACHE_E4M3)
+    return cache->head_dim == 64 ? shared_rows<64, true>(c, a, G, o, ms, s)
+                                 : shared_rows<128, true>(c, a, G, o, ms, s);
+  return cache->head_dim == 64 ? shared_rows<64, false>(c, a, G, o, ms, s)
+                               : shared_rows<128, false>(c, a, G, o, ms, s);
 }
 
 struct PrefixLayout {
-  size_t eff, groups, tiles, part_o, part_ms, total;
+  size_t seqs, groups, cut, nodes, share_o, share_ms, part_o, part_ms, total;
 };
 
 // The call's sizes, and its workspace; false: sizes out of range.
@@ -163,26 +170,32 @@ bool prefix_layout(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int
                    int64_t G, PrefixLayout &l) {
   if (!attn_sizes_ok(B, T, Hq, Hkv, D, room) || G < 0 || G > B) return false;
   const int64_t group = Hq / Hkv;
-  int parts = attn_plan(B, T, Hq, Hkv, D, room).S;
   size_t off = 0;
   l = PrefixLayout{};
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
   if (G > 0) {
     if (B * T >= ((int64_t)1 << 31) / group) return false;
-    const AttnPlan p = share_plan(B, T, Hq, Hkv, D, room, G);
-    const int64_t units = (int64_t)Hkv * p.S;
-    if (!grid_ok((units + 7) / 8 * 8 * p.m_tiles, 1024)) return false;
-    parts += p.S;
-    off = align_up((size_t)B * sizeof(int32_t));
-    l.groups = off;
-    off = align_up(off + (size_t)G * sizeof(ShareGroup));
-    l.tiles = off;
-    off = align_up(off + (size_t)p.m_tiles * sizeof(ShareTile));
+    const int64_t rows = share_rows(B, T, group);
+    // every unit, and every piece of the line, begins a part at most
+    const int64_t units = (B * T * group / rows + G) * Hkv;
+    if (units >= (int64_t)1 << 30) return false;
+    const size_t parts = (size_t)(units + kShareWorkgroups) * rows;
+    l.seqs = take((size_t)B * sizeof(ShareSeq));
+    l.groups = take((size_t)G * sizeof(ShareGroup));
+    l.cut = take(sizeof(ShareCut));
+    l.nodes = take((size_t)(B * T) * sizeof(int32_t));
+    l.share_o = take(parts * D * sizeof(float));
+    l.share_ms = take(parts * 2 * sizeof(float));
   }
-  l.part_o = off;
-  if (parts > 1) {
-    const size_t rows = (size_t)(B * T) * Hq;
-    l.part_ms = off + attn_ms_offset(rows, parts, D);
-    off = align_up(l.part_ms + rows * parts * 2 * sizeof(float));
+  const int S = attn_plan(B, T, Hq, Hkv, D, room).S;
+  if (S > 1) {
+    const size_t rows = (size_t)(B * T) * Hq * S;
+    l.part_o = take(rows * D * sizeof(float));
+    l.part_ms = take(rows * 2 * sizeof(float));
   }
   l.total = std::max(off, kAlign);
   return true;
@@ -374,12 +387,10 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
   a.depth = anc ? depth : nullptr;  // a chain's depths are its nodes' numbers
   a.part_o = reinterpret_cast<float *>(ws + l.part_o);
   a.part_ms = reinterpret_cast<float *>(ws + l.part_ms);
-  const bool shaped = cap > 0.0f || slopes;
   const AttnPlan own = attn_plan(B, T, q_heads, c.Hkv, D, room);
-  a.parts = own.S;
+  attn_split(a, own, B * c.Hkv * own.S);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (n_groups > 0) {
-    const AttnPlan p = share_plan(B, T, q_heads, c.Hkv, D, room, n_groups);
     ShareArgs sh;
     sh.off = share_off;
     sh.ctx_len = ctx_len;
@@ -392,27 +403,33 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
     sh.max_pages = c.max_pages;
     sh.page_shift = c.page_shift;
     sh.group = a.group;
-    sh.m_rows = p.m_rows;
-    sh.m_tiles = p.m_tiles;
-    sh.eff = reinterpret_cast<int32_t *>(ws + l.eff);
+    sh.heads = c.Hkv;
+    sh.m_rows = share_rows(B, T, a.group);
+    sh.tile = kSharedTile;
+    sh.seqs = reinterpret_cast<ShareSeq *>(ws + l.seqs);
+    sh.nodes = reinterpret_cast<int32_t *>(ws + l.nodes);
     sh.groups = reinterpret_cast<ShareGroup *>(ws + l.groups);
-    sh.tiles = reinterpret_cast<ShareTile *>(ws + l.tiles);
+    sh.cut = reinterpret_cast<ShareCut *>(ws + l.cut);
     CallTimer tm;
     SVD_LAUNCH(tm, SVD_KERNEL_SHARE, s, kr_share, dim3((unsigned)n_groups), dim3(kShareBlock), s,
                sh);
-    a.eff = sh.eff;
+    if (n_groups > 1)
+      SVD_LAUNCH(tm, SVD_KERNEL_SHARE, s, kr_share_cut, dim3(1), dim3(kShareBlock), s, sh);
+    a.seqs = sh.seqs;
     a.groups = sh.groups;
-    a.tiles = sh.tiles;
-    a.parts = own.S + p.S;
-    attn_split(a, p, (int64_t)c.Hkv * p.S);
-    rc = shaped ? attn_kind<kSharedShaped>(cache, p, c, a, q_heads, s)
-                : attn_kind<kShared>(cache, p, c, a, q_heads, s);
+    a.cut = sh.cut;
+    a.nodes = sh.nodes;
+    a.share_rows = sh.m_rows;
+    float *const o = reinterpret_cast<float *>(ws + l.share_o);
+    float *const ms = reinterpret_cast<float *>(ws + l.share_ms);
+    a.share_o = o;
+    a.share_ms = ms;
+    rc = shared_kind(cache, c, a, n_groups, o, ms, s);
     if (rc != SVD_OK) return rc;
-    a.part0 = p.S;
+  } else if (cap == 0.0f && !slopes) {
+    return attn_kind<kTree>(cache, own, c, a, q_heads, s);
   }
-  attn_split(a, own, B * c.Hkv * own.S);
-  if (n_groups > 0 || shaped) return attn_kind<kShaped>(cache, own, c, a, q_heads, s);
-  return attn_kind<kTree>(cache, own, c, a, q_heads, s);
+  return attn_kind<kShaped>(cache, own, c, a, q_heads, s);
 }
 
 }  // extern "C"

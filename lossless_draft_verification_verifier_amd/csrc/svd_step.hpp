@@ -209,7 +209,7 @@ int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   const int64_t grid = ((int64_t)a.units + 7) / 8 * 8 * a.m_tiles;
   SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ, WT, kForm>,
              dim3((unsigned)grid), dim3(AttnShape<D, kE4M3, NT, WQ, WT>::kBlock), s, c, a);
-  if (a.parts > 1 && a.part0 + a.S == a.parts) {  // the last of a row's parts
+  if (a.S > 1) {
     constexpr int rows = kAttnJoinBlock / (D / 4);
     SVD_LAUNCH(tm, SVD_KERNEL_ATTENTION_JOIN, s, kr_attn_join<D>,
                dim3((unsigned)((a.rows_all + rows - 1) / rows)), dim3(kAttnJoinBlock), s, a, Hq);
@@ -220,12 +220,10 @@ int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
 template <int D, bool kE4M3, int kForm>
 int attn_rows(const AttnPlan &p, const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   if (p.nt == 2 && p.wq == 8) return attn_launch<D, kE4M3, 2, 8, 1, kForm>(c, a, Hq, s);
-  if constexpr (kForm == kTree || kForm == kShaped) {  // the arrangements of a group's rows are fewer
-    if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 2, kForm>(c, a, Hq, s);
-    if (p.wq == 3) return attn_launch<D, kE4M3, 1, 3, 1, kForm>(c, a, Hq, s);
-    if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2, 2, kForm>(c, a, Hq, s);
-  }
+  if (p.nt == 2) return attn_launch<D, kE4M3, 2, 4, 2, kForm>(c, a, Hq, s);
   if (p.wq == 4) return attn_launch<D, kE4M3, 1, 4, 1, kForm>(c, a, Hq, s);
+  if (p.wq == 3) return attn_launch<D, kE4M3, 1, 3, 1, kForm>(c, a, Hq, s);
+  if (p.wq == 2) return attn_launch<D, kE4M3, 1, 2, 2, kForm>(c, a, Hq, s);
   return attn_launch<D, kE4M3, 1, 1, 2, kForm>(c, a, Hq, s);
 }
 
@@ -353,7 +351,6 @@ int svd_tree_attention(const svd_cache_t *cache, const void *q, int64_t q_stride
   const AttnPlan p = attn_plan(B, T, q_heads, c.Hkv, D, room);
   AttnArgs a = attn_args(c, q, q_stride, ctx_len, n_nodes, anc, cs, B, T, q_heads, out, lse);
   attn_split(a, p, B * c.Hkv * p.S);
-  a.parts = p.S;
   a.part_o = static_cast<float *>(workspace);
   a.part_ms = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                         attn_ms_offset(a.rows_all, p.S, D));
