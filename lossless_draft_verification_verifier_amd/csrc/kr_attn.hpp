@@ -199,14 +199,24 @@ __device__ __forceinline__ ShareRow share_row(const AttnArgs &a, int64_t b, int 
 template <int D>
 __device__ __forceinline__ void share_join(const AttnArgs &a, const ShareRow &r, int d, f32x4 &o,
                                            float &m, float &l) {
-  float mm = m;
-  for (int s = 0; s < r.n; ++s)
+  // one or two parts mostly: both on their way at once
+  const int64_t at0 = r.at, at1 = r.at + (r.n > 1 ? a.share_rows : 0);
+  const float m0 = a.share_ms[2 * at0], l0 = a.share_ms[2 * at0 + 1];
+  const float m1 = a.share_ms[2 * at1], l1 = r.n > 1 ? a.share_ms[2 * at1 + 1] : 0.0f;
+  const f32x4 o0 = *reinterpret_cast<const f32x4 *>(a.share_o + at0 * D + d);
+  const f32x4 o1 = *reinterpret_cast<const f32x4 *>(a.share_o + at1 * D + d);
+  float mm = fmaxf(fmaxf(m, m0), m1);
+  for (int s = 2; s < r.n; ++s)
     mm = fmaxf(mm, a.share_ms[2 * (r.at + (int64_t)s * a.share_rows)]);
-  const float f = part_factor(m, l, mm);
-  o *= f;
-  l *= f;
-#pragma unroll 2
-  for (int s = 0; s < r.n; ++s) {
+  const float f = part_factor(m, l, mm), f0 = part_factor(m0, l0, mm);
+  o = o * f + o0 * f0;
+  l = l * f + l0 * f0;
+  if (r.n > 1) {
+    const float f1 = part_factor(m1, l1, mm);
+    o += o1 * f1;
+    l += l1 * f1;
+  }
+  for (int s = 2; s < r.n; ++s) {
     const int64_t at = r.at + (int64_t)s * a.share_rows;
     const float ms = a.share_ms[2 * at], ls = a.share_ms[2 * at + 1];
     const float g = part_factor(ms, ls, mm);

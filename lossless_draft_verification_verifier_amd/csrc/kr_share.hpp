@@ -36,6 +36,7 @@ __device__ __forceinline__ void share_cut(ShareCut *cut, int64_t total) {
 __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
   __shared__ int lo_ok, n_act, first, ctx_min, pages;
   __shared__ int wave_sum[kShareBlock / 64];
+  __shared__ unsigned long long who[kShareBlock / 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t g = blockIdx.x;
   if (threadIdx.x == 0) {
@@ -70,21 +71,45 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
   if (threadIdx.x == 0) pages = cols;
   __syncthreads();
   if (cols > 0) {
-    // a wave per sequence, four columns of a lane at a time
+    // a wave has every 16th sequence, four of them and 256 columns at a time
     const int32_t *const one = a.table + (int64_t)f * a.max_pages;
-    for (int b = lo + w; b < hi; b += kShareBlock / 64) {
-      if (b == f || !active(b)) continue;
-      const int32_t *const other = a.table + (int64_t)b * a.max_pages;
-      for (int c0 = 0; c0 < pages; c0 += 256) {  // (pages only falls)
-        int least = cols;
+    for (int b0 = lo; b0 < hi; b0 += kShareBlock) {
+      // who is compared, of this stretch of sequences
+      const int mine = b0 + (int)threadIdx.x;
+      const unsigned long long act = __ballot(mine < hi && mine != f && active(mine));
+      if (lane == 0) who[w] = act;
+      __syncthreads();
+      // every thread takes the bound between two barriers with no change of it
+      for (int c0 = 0, c_end = pages; c0 < c_end; c0 += 256) {
+        __syncthreads();
+        int at[4], want[4];
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          const int c = c0 + 64 * i + lane, at = min(c, cols - 1);
-          if (one[at] != other[at]) least = at;
+        for (int i = 0; i < 4; ++i) {
+          at[i] = min(c0 + 64 * i + lane, cols - 1);
+          want[i] = one[at[i]];
+        }
+        int least = cols;
+        for (int k = w; k < kShareBlock && b0 + k < hi; k += 4 * (kShareBlock / 64)) {
+          int got[4][4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int b = k + s * (kShareBlock / 64);
+            const bool on = b < kShareBlock && b0 + b < hi && (who[b >> 6] >> (b & 63) & 1);
+            const int32_t *const row = on ? a.table + (int64_t)(b0 + b) * a.max_pages : one;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) got[s][i] = row[at[i]];
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 3; i >= 0; --i)
+              if (got[s][i] != want[i]) least = min(least, at[i]);
         }
         if (least < cols) atomicMin(&pages, least);
-        if (__any(least < cols)) break;
+        __syncthreads();
+        c_end = pages;
       }
+      __syncthreads();
     }
   }
   __syncthreads();

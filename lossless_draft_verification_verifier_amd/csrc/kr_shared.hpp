@@ -6,13 +6,19 @@
 //   S^T = K Q^T     v_mfma_f32_32x32x16_bf16, 32 tokens x 32 rows
 //   p = exp2(S c - m c)
 //   O^T += V^T P^T  the same instruction, 32 head elements x 32 rows
-// A lane keeps one row of each 32, half of the tokens of a product's block; p leaves the
-// first product in the order in which the second one takes it.  A wave has 32 * RB rows
-// (RB = 2: every key and value fragment it reads from LDS serves two products, which halves
-// what bounds the tree's kernel), four waves a workgroup, one workgroup per CU and all the
-// registers of a SIMD for its wave.  There is no second wave to hide a wait, so the steps
-// are laid side by side: while a block of 32 tokens' scores are exponentiated, the next
-// block's scores are computed, and its own values meet their p one block later.
+// A lane keeps one row of 32 and half of the tokens of a product's block; p leaves the
+// first product in the order in which the second one takes it.  A wave has 32 rows, eight
+// waves a workgroup, two a SIMD, one workgroup per CU.  With 16 rows of a wave the reads of
+// K and V from LDS are what bounds it (141 us for 1024 nodes of 8 query heads over 4096
+// shared tokens of 8 kv heads), with 64 rows and one wave per SIMD the issue of one wave's
+// instructions (125 us); 32 rows and two waves take 92 us, 40% of the rate of the matrix
+// instructions alone.
+// Inside a wave the steps are laid side by side: a block of 32 tokens is exponentiated
+// while the next block's scores are computed, and its values meet their p a block later,
+// while the maxima of the next one are taken.
+//
+// Few rows (64 at most, of one group's sequences) leave six of the eight waves idle; then
+// four waves share 64 rows, two and two with half of the tokens each.
 //
 // K and V tiles lie in LDS as they are in memory, bf16 rows (widened on the way from E4M3,
 // exactly); V^T comes from a transposing read, four tokens of one head element per lane.
@@ -31,12 +37,13 @@ namespace svd {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kSharedBlock = 256;
 constexpr int kSharedTile = 64;      // tokens
 
-template <int D, int RB, int WT>
+// NW waves of 32 rows, WT of them with the same rows and other tokens.
+template <int D, int NW, int WT>
 struct SharedShape {
-  static constexpr int M = 4 / WT * RB * 32;             // rows of a workgroup
+  static constexpr int kBlock = 64 * NW;
+  static constexpr int M = NW / WT * 32;                 // rows of a workgroup
   static constexpr int SUB = 2 / WT;                     // blocks of 32 tokens per wave and tile
   static constexpr int NB = SUB == 2 ? 3 : 4;            // tiles in LDS
   static constexpr int kTile = kSharedTile * D * 2;      // bytes of K, or of V
@@ -55,19 +62,37 @@ __device__ __forceinline__ float half_max(float x) {
   return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
-template <int D, bool kE4M3, int RB, int WT, bool kShape>
-__global__ __launch_bounds__(kSharedBlock, 1) void kr_shared_attention(CacheView cv, AttnArgs a,
+// How scores become base-2 logarithms: scaled, or capped; and less what the distance takes.
+enum SharedScores { kPlain = 0, kCapped = 1, kSloped = 2, kCappedSloped = 3 };
+
+// The order in which a stretch of code issues: N times two products, `valu` vector
+// instructions beside them, and the LDS reads of the products three turns later.
+template <int N, int kReads, int kValu>
+__device__ __forceinline__ void beside_products() {
+  __builtin_amdgcn_sched_group_barrier(0x100, 3 * kReads, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);
+    if (i + 3 < N) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+  }
+}
+
+template <int D, bool kE4M3, int NW, int WT, int kScores>
+__global__ __launch_bounds__(64 * NW, NW / 4) void kr_shared_attention(CacheView cv, AttnArgs a,
                                                                        int64_t G, float *part_o,
                                                                        float *part_ms) {
-  using Shape = SharedShape<D, RB, WT>;
+  using Shape = SharedShape<D, NW, WT>;
+  constexpr int kBlock = Shape::kBlock;
+  constexpr bool kShape = kScores != kPlain;
   constexpr int M = Shape::M, SUB = Shape::SUB, NB = Shape::NB;
   constexpr int TK = kSharedTile, ST = D / 16, DT = D / 32;
   constexpr int RowB = D * 2;                         // bytes of a row in LDS
   constexpr int E = kE4M3 ? 16 : 8;                   // elements of a 16-byte load
   constexpr int PC = D / E;                           // loads of a token
-  constexpr int L = TK * PC / kSharedBlock;           // loads of a thread, of K and of V
-  constexpr int TL = kSharedBlock / PC;               // tokens of a round of loads
-  static_assert(L >= 1 && TL >= 8 && TL / 4 <= 16, "a wave's tokens are in one page");
+  constexpr int L = TK * PC > kBlock ? TK * PC / kBlock : 1;  // loads of a thread, of K and of V
+  constexpr int TL = kBlock / PC;                     // tokens of a round of loads
+  static_assert(64 / PC <= 16, "a wave's tokens are in one page");
   __shared__ __align__(16) unsigned char lds[Shape::kLds];
   __shared__ float lds_ms[WT > 1 ? WT : 1][WT > 1 ? M : 1][2];
   unsigned char *const ldk = lds, *const ldv = lds + NB * Shape::kTile;
@@ -91,9 +116,10 @@ __global__ __launch_bounds__(kSharedBlock, 1) void kr_shared_attention(CacheView
   for (int i = 0; i < DT; ++i)
     v_at[i] = vt * RowB + (((2 * i + ((lane >> 4) & 1)) ^ vx) << 5) + ((vi & 3) << 3);
   // where a thread writes, and what it loads: piece tid % PC of token tid / PC + round * TL
-  const int s_tok = tid / PC, s_pc = tid % PC;
+  const int s_tok = tid / PC % TK, s_pc = tid % PC;
+  const bool loads = TK * PC >= kBlock || tid < TK * PC;
   const uint32_t in_page = (1u << cv.page_shift) - 1;
-  constexpr uint32_t RB_ = kE4M3 ? D : 2 * D;  // bytes of a cached row
+  constexpr uint32_t Row = kE4M3 ? D : 2 * D;  // bytes of a cached row
   const uint32_t page_rows = (uint32_t)cv.Hkv << cv.page_shift;
 
   for (int64_t pos = piece * per; pos < end;) {
@@ -120,49 +146,52 @@ __global__ __launch_bounds__(kSharedBlock, 1) void kr_shared_attention(CacheView
     const uint32_t head_row = (uint32_t)h << cv.page_shift;
     pos += t_hi - t_lo;
 
-    vec16 qf[RB][ST];
-    int at_row[RB];
-    float slope[RB];
+    vec16 qf[ST];
+    const int r = min(r_lo + wq * 32 + n, rows - 1);
+    const int64_t token = list[r / a.group];
+    const int head = h * a.group + r % a.group;
+    const uint16_t *q = a.q + token * a.q_stride + (int64_t)head * D + 8 * half;
 #pragma unroll
-    for (int t = 0; t < RB; ++t) {
-      const int r = min(r_lo + (wq * RB + t) * 32 + n, rows - 1);
-      const int64_t token = list[r / a.group];
-      const int head = h * a.group + r % a.group;
-      const uint16_t *q = a.q + token * a.q_stride + (int64_t)head * D + 8 * half;
-#pragma unroll
-      for (int i = 0; i < ST; ++i) qf[t][i] = *reinterpret_cast<const vec16 *>(q + 16 * i);
-      at_row[t] = 0;
-      slope[t] = 0.0f;
-      if (kShape && a.slopes) {
-        at_row[t] = a.ctx_len[token / a.T] + (a.depth ? a.depth[token] : (int)(token % a.T));
-        slope[t] = a.slopes[head] * 1.4426950408889634f;
-      }
+    for (int i = 0; i < ST; ++i) qf[i] = *reinterpret_cast<const vec16 *>(q + 16 * i);
+    int at_row = 0;
+    float slope = 0.0f;
+    if constexpr ((kScores & kSloped) != 0) {
+      at_row = a.ctx_len[token / a.T] + (a.depth ? a.depth[token] : (int)(token % a.T));
+      slope = a.slopes[head] * 1.4426950408889634f;
     }
 
     vec16 rk[L], rv[L];
     uint32_t sk[L], sv[L];
-    int ok = 0;
-    auto load_tile = [&](int tile) {
-      ok = 0;
-      if (tile >= t_hi) return;
+    int ok = 0, pages[L];
+    // the table's entries for a tile go out a tile before its loads, which wait for them
+    auto load_pages = [&](int tile) {
 #pragma unroll
       for (int j = 0; j < L; ++j) {
-        const uint32_t p = (uint32_t)tile * TK + j * TL + s_tok;
-        const int pg = table[__builtin_amdgcn_readfirstlane(p >> cv.page_shift)];
+        const uint32_t p = (uint32_t)min(tile, t_hi - 1) * TK + j * TL + s_tok;
+        pages[j] = table[__builtin_amdgcn_readfirstlane(p >> cv.page_shift)];
+      }
+    };
+    auto load_tile = [&](int tile) {  // behind the last tile: that one again
+      ok = 0;
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        const uint32_t p = (uint32_t)min(tile, t_hi - 1) * TK + j * TL + s_tok;
+        const int pg = pages[j];
         const bool good = (uint32_t)pg < (uint32_t)cv.n_pages;
         ok |= good << j;
         const uint32_t at = head_row + (p & in_page);
         const uint64_t row = (uint64_t)(good ? pg : 0) * page_rows;
-        rk[j] = *reinterpret_cast<const vec16 *>(cv.k + row * RB_ + (at * RB_ + s_pc * 16));
-        rv[j] = *reinterpret_cast<const vec16 *>(cv.v + row * RB_ + (at * RB_ + s_pc * 16));
+        rk[j] = *reinterpret_cast<const vec16 *>(cv.k + row * Row + (at * Row + s_pc * 16));
+        rv[j] = *reinterpret_cast<const vec16 *>(cv.v + row * Row + (at * Row + s_pc * 16));
         if constexpr (kE4M3) {
           sk[j] = cv.k_scale[row + at];
           sv[j] = cv.v_scale[row + at];
         }
       }
+      load_pages(tile + 1);
     };
-    auto store_tile = [&](int tile, int buf) {
-      if (tile >= t_hi) return;
+    auto store_tile = [&](int buf) {
+      if (!loads) return;
 #pragma unroll
       for (int j = 0; j < L; ++j) {
         const int tok = j * TL + s_tok;
@@ -197,30 +226,21 @@ __global__ __launch_bounds__(kSharedBlock, 1) void kr_shared_attention(CacheView
       }
     };
 
-    f32x16 o[RB][DT], sc[RB];
-    float base[RB], l[RB];
-    vec16 pf[RB][2];
+    f32x16 o[DT], sc;
+    float base = kNegInf, l = 0.0f;
+    vec16 pf[2];
 #pragma unroll
-    for (int t = 0; t < RB; ++t) {
-      base[t] = kNegInf;
-      l[t] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) o[t][i] = f32x16{};
-    }
+    for (int i = 0; i < DT; ++i) o[i] = f32x16{};
     // the scores of a block of 32 tokens; a block's values with its p
     auto scores = [&](int buf, int sub) {
       const unsigned char *const p = ldk + buf * Shape::kTile + sub * 32 * RowB;
-      f32x16 s[RB];
-#pragma unroll
-      for (int t = 0; t < RB; ++t) s[t] = f32x16{};
+      f32x16 s = {};
 #pragma unroll
       for (int i = 0; i < ST; ++i) {
         const vec16 kf = *reinterpret_cast<const vec16 *>(p + (k_at ^ (i << 5)));
-#pragma unroll
-        for (int t = 0; t < RB; ++t) s[t] = mfma32(kf, qf[t][i], s[t]);
+        s = mfma32(kf, qf[i], s);
       }
-#pragma unroll
-      for (int t = 0; t < RB; ++t) sc[t] = s[t];
+      sc = s;
     };
     auto values = [&](int buf, int sub) {
       const unsigned char *const p = ldv + buf * Shape::kTile + sub * 32 * RowB;
@@ -234,120 +254,94 @@ __global__ __launch_bounds__(kSharedBlock, 1) void kr_shared_attention(CacheView
           const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(q + 8 * RowB));
           const u32x2 x2 = __builtin_bit_cast(u32x2, x), y2 = __builtin_bit_cast(u32x2, y);
           const vec16 vf = {x2.x, x2.y, y2.x, y2.y};
-#pragma unroll
-          for (int t = 0; t < RB; ++t) o[t][i] = mfma32(vf, pf[t][w], o[t][i]);
+          o[i] = mfma32(vf, pf[w], o[i]);
         }
     };
-    // what the exponentials need of a block's scores: the exponent moves when one passes it by
-    // 2^8, so most blocks rescale nothing
     const float cs = kShape ? 1.0f : a.c;
     auto shape = [&](int tile, int sub) {
-      if constexpr (kShape) {
-        if (a.cap_in > 0.0f) {
+      const int p0 = tile * TK + sub * 32 + 4 * half;
+      const float from = (float)(p0 - at_row);
 #pragma unroll
-          for (int t = 0; t < RB; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sc[t][r] = capped(sc[t][r], a.cap_in, a.cap_out);
-        } else {
-#pragma unroll
-          for (int t = 0; t < RB; ++t) sc[t] *= a.c;
-        }
-        if (a.slopes) {
-          const int p0 = tile * TK + sub * 32 + 4 * half;
-#pragma unroll
-          for (int t = 0; t < RB; ++t) {
-            const float from = (float)(p0 - at_row[t]);
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              sc[t][r] = __builtin_fmaf(slope[t], from + (float)(8 * (r / 4) + r % 4), sc[t][r]);
-          }
-        }
+      for (int r = 0; r < 16; ++r) {
+        sc[r] = kScores & kCapped ? capped(sc[r], a.cap_in, a.cap_out) : sc[r] * a.c;
+        if constexpr ((kScores & kSloped) != 0)
+          sc[r] = __builtin_fmaf(slope, from + (float)(8 * (r / 4) + r % 4), sc[r]);
       }
     };
-    auto move = [&] {
-      float next[RB];
-      bool moves = false;
+    // A block of 32 tokens: the values of the block before (from vb) beside this one's maxima,
+    // the next one's scores (from kb) beside this one's exponentials.  The exponent moves
+    // when a score passes it by 2^8, so most blocks rescale nothing.
+    auto block = [&](auto with_values, int tile, int sub, int vb, int vsub, int kb, int ksub) {
+      if constexpr (with_values.value) values(vb, vsub);
+      if constexpr (kShape) shape(tile, sub);
+      float mx = sc[0];
 #pragma unroll
-      for (int t = 0; t < RB; ++t) {
-        float mx = sc[t][0];
+      for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[r]);
+      const float next = half_max(mx) * cs;
+      const bool up = next > base + 8.0f;
+      // vector instructions beside two products: those of the shape and the maxima
+      constexpr int kShapeOps = kScores & kCapped ? 24 : 4, kSlopeOps = kScores & kSloped ? 8 : 0;
+      if constexpr (with_values.value) beside_products<DT, 4, kShapeOps + kSlopeOps>();
+      if (__any(up)) {
+        const float f = up ? fast_exp2(base - next) : 1.0f;
+        l *= f;
 #pragma unroll
-        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[t][r]);
-        next[t] = half_max(mx) * cs;
-        moves |= next[t] > base[t] + 8.0f;
+        for (int i = 0; i < DT; ++i) o[i] *= f;
+        base = up ? next : base;
       }
-      if (__any(moves)) {
+      f32x16 p = sc;
+      scores(kb, ksub);
+      const float less = base == kNegInf ? 0.0f : base;
 #pragma unroll
-        for (int t = 0; t < RB; ++t) {
-          const bool up = next[t] > base[t] + 8.0f;
-          const float f = up ? fast_exp2(base[t] - next[t]) : 1.0f;
-          l[t] *= f;
-#pragma unroll
-          for (int i = 0; i < DT; ++i) o[t][i] *= f;
-          base[t] = up ? next[t] : base[t];
-        }
+      for (int r = 0; r < 16; ++r) {
+        p[r] = fast_exp2(__builtin_fmaf(p[r], cs, -less));
+        l += p[r];
       }
-    };
-    auto weights = [&] {
 #pragma unroll
-      for (int t = 0; t < RB; ++t) {
-        const float sub = base[t] == kNegInf ? 0.0f : base[t];
-        float p[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          p[r] = fast_exp2(__builtin_fmaf(sc[t][r], cs, -sub));
-          l[t] += p[r];
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          pf[t][w] = vec16{pack_bf16(p[8 * w], p[8 * w + 1]), pack_bf16(p[8 * w + 2], p[8 * w + 3]),
-                           pack_bf16(p[8 * w + 4], p[8 * w + 5]),
-                           pack_bf16(p[8 * w + 6], p[8 * w + 7])};
-      }
+      for (int w = 0; w < 2; ++w)
+        pf[w] = vec16{pack_bf16(p[8 * w], p[8 * w + 1]),
+                      pack_bf16(p[8 * w + 2], p[8 * w + 3]),
+                      pack_bf16(p[8 * w + 4], p[8 * w + 5]),
+                      pack_bf16(p[8 * w + 6], p[8 * w + 7])};
+      beside_products<ST / 2, 2, 128 / ST>();
     };
 
     __syncthreads();  // the piece before is done with LDS
+    load_pages(t_lo);
     load_tile(t_lo);
-    store_tile(t_lo, 0);
+    store_tile(0);
     load_tile(t_lo + 1);
     __syncthreads();
     scores(0, SUB == 2 ? 0 : wt);
-    int buf = 0, last_buf = 0;  // of this tile, and of the one before
-    for (int tile = t_lo; tile < t_hi; ++tile) {
+    // Behind the last tile there are scores of whatever LDS holds, which nothing uses.
+    int buf = 0, last = 0;  // where this tile is, and the one before
+    auto tile_of = [&](auto with_values, int tile) {
       const int next = buf + 1 == NB ? 0 : buf + 1;
-      store_tile(tile + 1, next);
+      store_tile(next);
       load_tile(tile + 2);
-      if constexpr (SUB == 1) __syncthreads();  // the next tile is there
-#pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        const int sub = SUB == 2 ? s : wt;
-        shape(tile, sub);
-        if (s) values(buf, 0);
-        else if (tile > t_lo) values(last_buf, SUB == 2 ? 1 : wt);
-        move();
-        weights();
-        if (SUB == 2 && s == 0) {
-          scores(buf, 1);
-          __syncthreads();  // the next tile is there, and the last one's values are done with
-        } else if (tile + 1 < t_hi) {
-          scores(next, SUB == 2 ? 0 : wt);
-        }
+      if constexpr (SUB == 2) {
+        block(with_values, tile, 0, last, 1, buf, 1);
+        __syncthreads();  // the next tile is there, and the last one's values are done with
+        block(std::true_type{}, tile, 1, buf, 0, next, 0);
+      } else {
+        __syncthreads();
+        block(with_values, tile, wt, last, wt, next, wt);
       }
-      last_buf = buf;
+      last = buf;
       buf = next;
-    }
-    values(last_buf, SUB == 2 ? 1 : wt);
+    };
+    tile_of(std::false_type{}, t_lo);
+    for (int tile = t_lo + 1; tile < t_hi; ++tile) tile_of(std::true_type{}, tile);
+    values(last, SUB == 2 ? 1 : wt);
 
-#pragma unroll
-    for (int t = 0; t < RB; ++t) l[t] += __shfl_xor(l[t], 32, 64);
+    l += __shfl_xor(l, 32, 64);
     if constexpr (WT == 1) {
-#pragma unroll
-      for (int t = 0; t < RB; ++t) {
-        const int R = (wq * RB + t) * 32 + n;
-        if (r_lo + R >= rows) continue;
-        const int64_t at = slot * M + R;
+      const int R = wq * 32 + n;
+      const int64_t at = slot * M + R;
+      if (r_lo + R < rows) {
         if (half == 0) {
-          part_ms[2 * at] = base[t];
-          part_ms[2 * at + 1] = l[t];
+          part_ms[2 * at] = base;
+          part_ms[2 * at + 1] = l;
         }
         float *const to = part_o + at * D + 4 * half;
 #pragma unroll
@@ -355,28 +349,25 @@ __global__ __launch_bounds__(kSharedBlock, 1) void kr_shared_attention(CacheView
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<f32x4 *>(to + 32 * i + 8 * q) =
-                f32x4{o[t][i][4 * q], o[t][i][4 * q + 1], o[t][i][4 * q + 2], o[t][i][4 * q + 3]};
+                f32x4{o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]};
       }
     } else {
       // the waves that split the tokens join over the largest exponent
       __syncthreads();
       float (*lo)[M][D + 4] = reinterpret_cast<float (*)[M][D + 4]>(lds);
-#pragma unroll
-      for (int t = 0; t < RB; ++t) {
-        const int R = (wq * RB + t) * 32 + n;
-        if (half == 0) {
-          lds_ms[wt][R][0] = base[t];
-          lds_ms[wt][R][1] = l[t];
-        }
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4 *>(&lo[wt][R][32 * i + 8 * q + 4 * half]) =
-                f32x4{o[t][i][4 * q], o[t][i][4 * q + 1], o[t][i][4 * q + 2], o[t][i][4 * q + 3]};
+      const int R = wq * 32 + n;
+      if (half == 0) {
+        lds_ms[wt][R][0] = base;
+        lds_ms[wt][R][1] = l;
       }
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4 *>(&lo[wt][R][32 * i + 8 * q + 4 * half]) =
+              f32x4{o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]};
       __syncthreads();
-      for (int i = tid; i < M * (D / 4); i += kSharedBlock) {
+      for (int i = tid; i < M * (D / 4); i += kBlock) {
         const int R = i / (D / 4), d = i % (D / 4) * 4;
         if (r_lo + R >= rows) break;
         float mm = kNegInf, ll = 0.0f;

@@ -128,28 +128,30 @@ int filter_rows(const void *logits, void *out, const FilterArgs &a, int64_t rows
 // Rows of a workgroup of the shared part: 256, or 64 with the tokens split over its waves
 // where there are no more.
 int share_rows(int64_t B, int32_t T, int64_t group) {
-  return B * T * group <= 64 ? SharedShape<128, 1, 2>::M : SharedShape<128, 2, 1>::M;
+  return B * T * group <= 64 ? SharedShape<128, 4, 2>::M : SharedShape<128, 8, 1>::M;
 }
 
-template <int D, bool kE4M3, int RB, int WT>
+template <int D, bool kE4M3, int NW, int WT>
 int shared_launch(const CacheView &c, const AttnArgs &a, int64_t G, float *o, float *ms,
                   hipStream_t s) {
   CallTimer tm;
-  if (a.cap_in > 0.0f || a.slopes) {
-    SVD_LAUNCH(tm, SVD_KERNEL_SHARED_ATTENTION, s, kr_shared_attention<D, kE4M3, RB, WT, true>,
-               dim3(kShareWorkgroups), dim3(kSharedBlock), s, c, a, G, o, ms);
-  } else {
-    SVD_LAUNCH(tm, SVD_KERNEL_SHARED_ATTENTION, s, kr_shared_attention<D, kE4M3, RB, WT, false>,
-               dim3(kShareWorkgroups), dim3(kSharedBlock), s, c, a, G, o, ms);
-  }
-  return SVD_OK;
+  auto go = [&](auto *kernel) -> int {
+    SVD_LAUNCH(tm, SVD_KERNEL_SHARED_ATTENTION, s, kernel, dim3(kShareWorkgroups),
+               dim3(64 * NW), s, c, a, G, o, ms);
+    return SVD_OK;
+  };
+  if (a.slopes)
+    return a.cap_in > 0.0f ? go(kr_shared_attention<D, kE4M3, NW, WT, kCappedSloped>)
+                           : go(kr_shared_attention<D, kE4M3, NW, WT, kSloped>);
+  return a.cap_in > 0.0f ? go(kr_shared_attention<D, kE4M3, NW, WT, kCapped>)
+                         : go(kr_shared_attention<D, kE4M3, NW, WT, kPlain>);
 }
 
 template <int D, bool kE4M3>
 int shared_rows(const CacheView &c, const AttnArgs &a, int64_t G, float *o, float *ms,
                 hipStream_t s) {
-  return a.share_rows == 64 ? shared_launch<D, kE4M3, 1, 2>(c, a, G, o, ms, s)
-                            : shared_launch<D, kE4M3, 2, 1>(c, a, G, o, ms, s);
+  return a.share_rows == 64 ? shared_launch<D, kE4M3, 4, 2>(c, a, G, o, ms, s)
+                            : shared_launch<D, kE4M3, 8, 1>(c, a, G, o, ms, s);
 }
 
 int shared_kind(const svd_cache_t *cache, const CacheView &c, const AttnArgs &a, int64_t G,
