@@ -256,15 +256,17 @@ struct AttnShape {
   static constexpr int kLdsBytes = 2 * kTileBytes > kJoinBytes ? 2 * kTileBytes : kJoinBytes;
 };
 
-// What a kernel computes: a prefix's rows over all of its tokens; or the same behind the
-// tokens that its group shares (none without groups), with shaped scores where asked.
-enum AttnForm { kTree = 0, kShaped = 1 };
+// What a kernel computes: a prefix's rows over all of its tokens; or those behind the tokens
+// that its group shares; with scores that are capped or fall off with distance; or both.  Four
+// instances: with one for all of them, plain scores behind shared tokens took 184 us instead of
+// 175, and capped ones of 256 prefixes without groups 400 instead of 357.
+enum AttnForm { kTree = 0, kShares = 1, kShapes = 2 };
 
 template <int D, bool kE4M3, int NT, int WQ, int WT, int kForm>
 __global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
                              (AttnShape<D, kE4M3, NT, WQ, WT>::kMinWaves))
 void kr_tree_attention(CacheView cv, AttnArgs a) {
-  constexpr bool kShape = kForm == kShaped;
+  constexpr bool kShape = (kForm & kShapes) != 0, kShare = (kForm & kShares) != 0;
   using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
   constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
   constexpr bool kRoles = Shape::kRoles;
@@ -305,13 +307,13 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   const int total = bad ? 0 : ctx + nodes;
   // a sequence's room goes up to 2^31 - page: sums past its length are 64 bits
   const int all_tiles = (int)(((int64_t)total + TK - 1) / TK);
-  const int first = kShape && a.seqs && !bad ? a.seqs[b].eff / TK : 0;
+  const int first = kShare && !bad ? a.seqs[b].eff / TK : 0;
   const int per = (all_tiles - first + a.S - 1) / a.S;
   const int t_lo = first + s * per, t_hi = min(t_lo + per, all_tiles);
 
-  __shared__ ShareRow lds_share[kShape ? M : 1];
+  __shared__ ShareRow lds_share[kShare ? M : 1];
   if (threadIdx.x == 0) lds_odd = 0;
-  if (kShape && first && a.S == 1)
+  if (kShare && first && a.S == 1)
     for (int r = r_lo + (int)threadIdx.x; r < r_hi; r += Shape::kBlock)
       lds_share[r - r_lo] = share_row(a, b, r / a.group, r % a.group, h);
   __syncthreads();
@@ -730,7 +732,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
       }
     } else {
       // shared parts are there already: the row ends here
-      if (kShape && first) share_join<D>(a, lds_share[R - r_lo], d, x, mm, ll);
+      if (kShare && first) share_join<D>(a, lds_share[R - r_lo], d, x, mm, ll);
       attn_row_out<D>(a, row, d, x, mm, ll, d == 0);
     }
   };

@@ -71,7 +71,8 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
   if (threadIdx.x == 0) pages = cols;
   __syncthreads();
   if (cols > 0) {
-    // a wave has every 16th sequence, four of them and 256 columns at a time
+    // a wave has every 16th sequence, all of a stretch and 256 columns at a time
+    constexpr int kInFlight = 16;
     const int32_t *const one = a.table + (int64_t)f * a.max_pages;
     for (int b0 = lo; b0 < hi; b0 += kShareBlock) {
       // who is compared, of this stretch of sequences
@@ -89,10 +90,10 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
           want[i] = one[at[i]];
         }
         int least = cols;
-        for (int k = w; k < kShareBlock && b0 + k < hi; k += 4 * (kShareBlock / 64)) {
-          int got[4][4];
+        for (int k = w; k < kShareBlock && b0 + k < hi; k += kInFlight * (kShareBlock / 64)) {
+          int got[kInFlight][4];
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
+          for (int s = 0; s < kInFlight; ++s) {
             const int b = k + s * (kShareBlock / 64);
             const bool on = b < kShareBlock && b0 + b < hi && (who[b >> 6] >> (b & 63) & 1);
             const int32_t *const row = on ? a.table + (int64_t)(b0 + b) * a.max_pages : one;
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
             for (int i = 0; i < 4; ++i) got[s][i] = row[at[i]];
           }
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
+          for (int s = 0; s < kInFlight; ++s)
 #pragma unroll
             for (int i = 3; i >= 0; --i)
               if (got[s][i] != want[i]) least = min(least, at[i]);
@@ -136,20 +137,12 @@ __global__ __launch_bounds__(kShareBlock) void kr_share(ShareArgs a) {
   for (int b0 = lo; b0 < hi; b0 += kShareBlock) {
     const int b = b0 + (int)threadIdx.x;
     int n = 0, total;
-    if (b < hi) {
-      n = tokens && active(b) ? (a.n_nodes ? a.n_nodes[b] : a.T) : 0;
-    }
+    if (b < hi && tokens && active(b)) n = a.n_nodes ? a.n_nodes[b] : a.T;
     const int from = listed + scan(n, total) - n;
     listed += total;
     if (b < hi) a.seqs[b] = ShareSeq{n ? tokens : 0, (int32_t)g, from, 0};
-    // a wave's sequences, one after another
-    for (unsigned long long who = __ballot(n > 0); who; who &= who - 1) {
-      const int k = __builtin_ctzll(who);
-      const int kn = __builtin_amdgcn_readlane(n, k), kf = __builtin_amdgcn_readlane(from, k);
-      const int64_t kb = (int64_t)b0 + w * 64 + k;
-      for (int t = lane; t < kn; t += 64)
-        a.nodes[(int64_t)lo * a.T + kf + t] = (int32_t)(kb * a.T + t);
-    }
+    for (int i = 0; i < n; ++i)
+      a.nodes[(int64_t)lo * a.T + from + i] = (int32_t)((int64_t)b * a.T + i);
   }
   // sequences of no group
   const int64_t in_lo = valid ? a.off[0] : 0, in_hi = valid ? a.off[a.G] : 0;

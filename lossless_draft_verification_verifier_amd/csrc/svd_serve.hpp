@@ -428,10 +428,13 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
     a.share_ms = ms;
     rc = shared_kind(cache, c, a, n_groups, o, ms, s);
     if (rc != SVD_OK) return rc;
-  } else if (cap == 0.0f && !slopes) {
-    return attn_kind<kTree>(cache, own, c, a, q_heads, s);
   }
-  return attn_kind<kShaped>(cache, own, c, a, q_heads, s);
+  const bool shapes = cap > 0.0f || slopes;
+  if (n_groups > 0)
+    return shapes ? attn_kind<kShares | kShapes>(cache, own, c, a, q_heads, s)
+                  : attn_kind<kShares>(cache, own, c, a, q_heads, s);
+  return shapes ? attn_kind<kShapes>(cache, own, c, a, q_heads, s)
+                : attn_kind<kTree>(cache, own, c, a, q_heads, s);
 }
 
 }  // extern "C"
