@@ -199,24 +199,13 @@ __device__ __forceinline__ ShareRow share_row(const AttnArgs &a, int64_t b, int 
 template <int D>
 __device__ __forceinline__ void share_join(const AttnArgs &a, const ShareRow &r, int d, f32x4 &o,
                                            float &m, float &l) {
-  // one or two parts mostly: both on their way at once
-  const int64_t at0 = r.at, at1 = r.at + (r.n > 1 ? a.share_rows : 0);
-  const float m0 = a.share_ms[2 * at0], l0 = a.share_ms[2 * at0 + 1];
-  const float m1 = a.share_ms[2 * at1], l1 = r.n > 1 ? a.share_ms[2 * at1 + 1] : 0.0f;
-  const f32x4 o0 = *reinterpret_cast<const f32x4 *>(a.share_o + at0 * D + d);
-  const f32x4 o1 = *reinterpret_cast<const f32x4 *>(a.share_o + at1 * D + d);
-  float mm = fmaxf(fmaxf(m, m0), m1);
-  for (int s = 2; s < r.n; ++s)
+  float mm = m;
+  for (int s = 0; s < r.n; ++s)
     mm = fmaxf(mm, a.share_ms[2 * (r.at + (int64_t)s * a.share_rows)]);
-  const float f = part_factor(m, l, mm), f0 = part_factor(m0, l0, mm);
-  o = o * f + o0 * f0;
-  l = l * f + l0 * f0;
-  if (r.n > 1) {
-    const float f1 = part_factor(m1, l1, mm);
-    o += o1 * f1;
-    l += l1 * f1;
-  }
-  for (int s = 2; s < r.n; ++s) {
+  const float f = part_factor(m, l, mm);
+  l *= f;
+  o *= f;
+  for (int s = 0; s < r.n; ++s) {
     const int64_t at = r.at + (int64_t)s * a.share_rows;
     const float ms = a.share_ms[2 * at], ls = a.share_ms[2 * at + 1];
     const float g = part_factor(ms, ls, mm);
@@ -260,13 +249,13 @@ struct AttnShape {
 // that its group shares; with scores that are capped or fall off with distance; or both.  Four
 // instances: with one for all of them, plain scores behind shared tokens took 184 us instead of
 // 175, and capped ones of 256 prefixes without groups 400 instead of 357.
-enum AttnForm { kTree = 0, kShares = 1, kShapes = 2 };
+enum AttnForm { kTree = 0, kShaped = 1 };
 
 template <int D, bool kE4M3, int NT, int WQ, int WT, int kForm>
 __global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
                              (AttnShape<D, kE4M3, NT, WQ, WT>::kMinWaves))
 void kr_tree_attention(CacheView cv, AttnArgs a) {
-  constexpr bool kShape = (kForm & kShapes) != 0, kShare = (kForm & kShares) != 0;
+  constexpr bool kShape = kForm == kShaped;
   using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
   constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
   constexpr bool kRoles = Shape::kRoles;
@@ -307,13 +296,13 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   const int total = bad ? 0 : ctx + nodes;
   // a sequence's room goes up to 2^31 - page: sums past its length are 64 bits
   const int all_tiles = (int)(((int64_t)total + TK - 1) / TK);
-  const int first = kShare && !bad ? a.seqs[b].eff / TK : 0;
+  const int first = a.seqs && !bad ? a.seqs[b].eff / TK : 0;
   const int per = (all_tiles - first + a.S - 1) / a.S;
   const int t_lo = first + s * per, t_hi = min(t_lo + per, all_tiles);
 
-  __shared__ ShareRow lds_share[kShare ? M : 1];
+  __shared__ ShareRow lds_share[M];
   if (threadIdx.x == 0) lds_odd = 0;
-  if (kShare && first && a.S == 1)
+  if (first && a.S == 1)
     for (int r = r_lo + (int)threadIdx.x; r < r_hi; r += Shape::kBlock)
       lds_share[r - r_lo] = share_row(a, b, r / a.group, r % a.group, h);
   __syncthreads();
@@ -720,62 +709,70 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 
   __syncthreads();  // the parts of all waves are there
 
+  // What follows reads its arguments again: held in registers all the way, they spill the
+  // loop's own scalars (68 of them, 90 with shaped scores).
+  typedef __attribute__((address_space(4))) const char *kernarg;
+  kernarg late = (kernarg)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(late));
+  const CacheView &cz = *(const CacheView *)late;
+  const AttnArgs &az = *(const AttnArgs *)(late + (sizeof(CacheView) + 7) / 8 * 8);
+
   // one row's 4 elements from d on, its exponent and its sum
   auto put = [&](int R, int d, f32x4 x, float mm, float ll) {
-    const int64_t row = (b * a.T + R / a.group) * Hq + h * a.group + R % a.group;
-    if (a.S > 1) {
-      const int64_t pr = (int64_t)s * a.rows_all + row;
-      *reinterpret_cast<f32x4 *>(a.part_o + pr * D + d) = x;
+    const int64_t row = (b * az.T + R / az.group) * Hq + h * az.group + R % az.group;
+    if (az.S > 1) {
+      const int64_t pr = (int64_t)s * az.rows_all + row;
+      *reinterpret_cast<f32x4 *>(az.part_o + pr * D + d) = x;
       if (d == 0) {
-        a.part_ms[2 * pr] = mm;
-        a.part_ms[2 * pr + 1] = ll;
+        az.part_ms[2 * pr] = mm;
+        az.part_ms[2 * pr + 1] = ll;
       }
     } else {
       // shared parts are there already: the row ends here
-      if (kShare && first) share_join<D>(a, lds_share[R - r_lo], d, x, mm, ll);
-      attn_row_out<D>(a, row, d, x, mm, ll, d == 0);
+      if (first) share_join<D>(az, lds_share[R - r_lo], d, x, mm, ll);
+      attn_row_out<D>(az, row, d, x, mm, ll, d == 0);
     }
   };
   // what the tokens of this part whose values are not finite add to 4 elements
   auto odd_values = [&](int R, int d, f32x4 x, float mm) {
-    const int nd = R / a.group;
-    const uint16_t *q = a.q + (b * a.T + nd) * a.q_stride +
-                        (int64_t)(h * a.group + R % a.group) * D;
+    const int nd = R / az.group;
+    const uint16_t *q = az.q + (b * az.T + nd) * az.q_stride +
+                        (int64_t)(h * az.group + R % az.group) * D;
     // from the first tile whose values were looked at: it can begin with context, which
     // every row attends to
     const int64_t lo = (int64_t)max(t_lo, ctx / TK) * TK;
     const int64_t hi = min((int64_t)t_hi * TK, (int64_t)total);
     for (int64_t p = lo; p < hi; ++p) {
       const int i = (int)(p - ctx);
-      if (i >= 0 && (a.anc ? !((a.anc[(b * a.T + nd) * W + (i >> 5)] >> (i & 31)) & 1u) : i > nd))
+      if (i >= 0 && (az.anc ? !((az.anc[(b * az.T + nd) * W + (i >> 5)] >> (i & 31)) & 1u) : i > nd))
         continue;
-      const int64_t row = cache_row(cv, b, p, h);
+      const int64_t row = cache_row(cz, b, p, h);
       if (row < 0) continue;
       float v[4];
       bool odd = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = cache_element<kE4M3, D>(cv.v, cv.v_scale, row, d + e);
+        v[e] = cache_element<kE4M3, D>(cz.v, cz.v_scale, row, d + e);
         odd |= !(fabsf(v[e]) < __builtin_huge_valf());
       }
       if (!odd) continue;
       float z = 0.0f;
       for (int e = 0; e < D; ++e)
-        z += cache_element<kE4M3, D>(cv.k, cv.k_scale, row, e) * BF16::at(q, e);
+        z += cache_element<kE4M3, D>(cz.k, cz.k_scale, row, e) * BF16::at(q, e);
       const float sub = mm == kNegInf ? 0.0f : mm;
       float pt;
       if constexpr (kShape) {
-        z = a.cap_in > 0.0f ? capped(z, a.cap_in, a.cap_out) : z * a.c;
-        if (a.slopes) {
-          const int64_t token = b * a.T + nd;
-          const int to = ctx + (a.depth ? a.depth[token] : nd);
-          const int from = i >= 0 && a.depth ? ctx + a.depth[b * a.T + i] : (int)p;
-          z = __builtin_fmaf(a.slopes[h * a.group + R % a.group] * 1.4426950408889634f,
+        z = az.cap_in > 0.0f ? capped(z, az.cap_in, az.cap_out) : z * az.c;
+        if (az.slopes) {
+          const int64_t token = b * az.T + nd;
+          const int to = ctx + (az.depth ? az.depth[token] : nd);
+          const int from = i >= 0 && az.depth ? ctx + az.depth[b * az.T + i] : (int)p;
+          z = __builtin_fmaf(az.slopes[h * az.group + R % az.group] * 1.4426950408889634f,
                              (float)(from - to), z);
         }
         pt = fast_exp2(z - sub);
       } else {
-        pt = fast_exp2(__builtin_fmaf(z, a.c, -sub));
+        pt = fast_exp2(__builtin_fmaf(z, az.c, -sub));
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -62,8 +62,9 @@ __device__ __forceinline__ float half_max(float x) {
   return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
-// How scores become base-2 logarithms: scaled, or capped; and less what the distance takes.
-enum SharedScores { kPlain = 0, kCapped = 1, kSloped = 2, kCappedSloped = 3 };
+// How scores become base-2 logarithms: scaled; capped; or scaled or capped, as the call says,
+// and less what the distance takes.
+enum SharedScores { kPlain = 0, kCapped = 1, kSloped = 2 };
 
 // The order in which a stretch of code issues: N times two products, `valu` vector
 // instructions beside them, and the LDS reads of the products three turns later.
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kr_shared_attention(CacheView
     for (int i = 0; i < ST; ++i) qf[i] = *reinterpret_cast<const vec16 *>(q + 16 * i);
     int at_row = 0;
     float slope = 0.0f;
-    if constexpr ((kScores & kSloped) != 0) {
+    if constexpr (kScores == kSloped) {
       at_row = a.ctx_len[token / a.T] + (a.depth ? a.depth[token] : (int)(token % a.T));
       slope = a.slopes[head] * 1.4426950408889634f;
     }
@@ -260,11 +261,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kr_shared_attention(CacheView
     const float cs = kShape ? 1.0f : a.c;
     auto shape = [&](int tile, int sub) {
       const int p0 = tile * TK + sub * 32 + 4 * half;
-      const float from = (float)(p0 - at_row);
+      if (kScores == kCapped || a.cap_in > 0.0f) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        sc[r] = kScores & kCapped ? capped(sc[r], a.cap_in, a.cap_out) : sc[r] * a.c;
-        if constexpr ((kScores & kSloped) != 0)
+        for (int r = 0; r < 16; ++r) sc[r] = capped(sc[r], a.cap_in, a.cap_out);
+      } else {
+        sc *= a.c;
+      }
+      if constexpr (kScores == kSloped) {
+        const float from = (float)(p0 - at_row);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
           sc[r] = __builtin_fmaf(slope, from + (float)(8 * (r / 4) + r % 4), sc[r]);
       }
     };
@@ -280,8 +286,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kr_shared_attention(CacheView
       const float next = half_max(mx) * cs;
       const bool up = next > base + 8.0f;
       // vector instructions beside two products: those of the shape and the maxima
-      constexpr int kShapeOps = kScores & kCapped ? 24 : 4, kSlopeOps = kScores & kSloped ? 8 : 0;
-      if constexpr (with_values.value) beside_products<DT, 4, kShapeOps + kSlopeOps>();
+      constexpr int kOps = kScores == kPlain ? 4 : kScores == kCapped ? 24 : 12;
+      if constexpr (with_values.value) beside_products<DT, 4, kOps>();
       if (__any(up)) {
         const float f = up ? fast_exp2(base - next) : 1.0f;
         l *= f;

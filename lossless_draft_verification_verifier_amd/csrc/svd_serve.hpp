@@ -116,13 +116,11 @@ int filter_rows(const void *logits, void *out, const FilterArgs &a, int64_t rows
     }
     if (most <= 64 * step) return filter_held<E, 0>(logits, out, a, rows, s);
   }
+  if (a.V > kFilterSmall) return filter_passes<E, false, kFilterBlock>(logits, out, a, rows, s);
   const bool vec = a.V * es % 16 == 0 && ((uintptr_t)logits) % 16 == 0 &&
                    ((uintptr_t)out) % 16 == 0;
-  if (a.V <= kFilterSmall)
-    return vec ? filter_passes<E, true, 256>(logits, out, a, rows, s)
-               : filter_passes<E, false, 256>(logits, out, a, rows, s);
-  return vec ? filter_passes<E, true, kFilterBlock>(logits, out, a, rows, s)
-             : filter_passes<E, false, kFilterBlock>(logits, out, a, rows, s);
+  return vec ? filter_passes<E, true, 256>(logits, out, a, rows, s)
+             : filter_passes<E, false, 256>(logits, out, a, rows, s);
 }
 
 // Rows of a workgroup of the shared part: 256, or 64 with the tokens split over its waves
@@ -140,9 +138,7 @@ int shared_launch(const CacheView &c, const AttnArgs &a, int64_t G, float *o, fl
                dim3(64 * NW), s, c, a, G, o, ms);
     return SVD_OK;
   };
-  if (a.slopes)
-    return a.cap_in > 0.0f ? go(kr_shared_attention<D, kE4M3, NW, WT, kCappedSloped>)
-                           : go(kr_shared_attention<D, kE4M3, NW, WT, kSloped>);
+  if (a.slopes) return go(kr_shared_attention<D, kE4M3, NW, WT, kSloped>);
   return a.cap_in > 0.0f ? go(kr_shared_attention<D, kE4M3, NW, WT, kCapped>)
                          : go(kr_shared_attention<D, kE4M3, NW, WT, kPlain>);
 }
@@ -429,12 +425,8 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
     rc = shared_kind(cache, c, a, n_groups, o, ms, s);
     if (rc != SVD_OK) return rc;
   }
-  const bool shapes = cap > 0.0f || slopes;
-  if (n_groups > 0)
-    return shapes ? attn_kind<kShares | kShapes>(cache, own, c, a, q_heads, s)
-                  : attn_kind<kShares>(cache, own, c, a, q_heads, s);
-  return shapes ? attn_kind<kShapes>(cache, own, c, a, q_heads, s)
-                : attn_kind<kTree>(cache, own, c, a, q_heads, s);
+  return cap > 0.0f || slopes ? attn_kind<kShaped>(cache, own, c, a, q_heads, s)
+                              : attn_kind<kTree>(cache, own, c, a, q_heads, s);
 }
 
 }  // extern "C"
