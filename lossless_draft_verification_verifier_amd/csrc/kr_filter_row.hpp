@@ -19,6 +19,14 @@
 // NV > 0: the row's logits stay in registers, NV 16-byte pieces per thread (bf16 up to
 // 155641 tokens, one workgroup per CU), and memory is read once.  NV = 0: every pass reads
 // them again, which the 256 MB last-level cache serves.
+//
+// Bounds, on one MI355X.  2304 rows of 152064 bf16 logits, every prefix with settings of its
+// own: 1.40 GB in 306 us, 4.6 TB/s, for 285 at a copy's rate (the general passes: 1151).  One
+// round of 256 rows by time stamps: loads and counts 11 us, the scan of the counters 2, weights
+// 1, the cut 3, ties 7, the store 7.  516 rows of 100003 fp32 logits, top-p alone: 257 us, the
+// weights' exponentials (230 cycles per 64 tokens), three rounds (general: 783).  256 rows of
+// bf16, 8 draws each: 53 us, half of them the second look at every token's weight (general:
+// 236).  One row, one draw: 26 us (general: 163).
 #pragma once
 
 #include "kr_filter.hpp"

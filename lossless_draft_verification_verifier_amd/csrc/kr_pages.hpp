@@ -13,6 +13,11 @@
 //   kr_pages_move  a thread per table entry: copies it, grants it or returns it.
 //   kr_slots       packed tokens: a running sum over the batch in every workgroup, then a
 //                  search for each token's sequence.
+// One workgroup plans, since every place follows from sums over the whole batch and 1024
+// sequences are one round of it: 3.8 us for 8 sequences, 6.0 for 1024.  The move is bound by
+// its bytes only where the tables are wide: 16.8 MB in 6.7 us for 1024 rows of 2048 entries
+// (2.5 TB/s, out of the last-level cache in part), 2.0 us for 8 rows of 64.  kr_slots: 3.7 us
+// for a few tokens, 4.9 for 41000 of 32 sequences.
 #pragma once
 
 #include "kr_cache.hpp"

@@ -6,6 +6,10 @@
 // shares nothing.  What is shared is rounded down to kShareTokens, whole tiles of either
 // head size; the rest is each sequence's own, like everything where fewer than two
 // sequences share.  So a wrong grouping costs time and changes no result.
+//
+// Latency bounds it: a table entry is one load behind lengths, offsets and the first
+// sequence.  A single group of 4 sequences takes 6 us, of 256 with 64 pages in reach 14
+// (with four sequences of a wave on their way at a time instead of sixteen 18, with one 32).
 #pragma once
 
 #include "kr_attn.hpp"

@@ -205,3 +205,34 @@ def test_two_calls_at_once_and_replayed(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@DTYPES
+@lengths(1, 2, 7, 64, 511, 1000, 1003, 4097, 8191, 8192)
+def test_many_rows_of_small_vocabularies(dtype, V):
+    # more rows than are held at a time, with settings of their own
+    svd = require_gpu()
+    say(dtype, V)
+    g = np.random.default_rng(V)
+    B = 270
+    z = rows(g, B, 1, V, dtype)
+    t, k = g.uniform(0.3, 1.5, B), g.integers(0, 200, B)
+    p, least = g.uniform(0.3, 1.05, B), np.where(g.random(B) < 0.5, 0.0, g.uniform(0, 0.2, B))
+    check(svd, z, t, k, p, least, u=g.random((B, 2, 1)))
+
+
+@DTYPES
+@lengths(1009, 2048)
+@pytest.mark.parametrize("one", range(len(ODD)))
+def test_many_rows_out_of_the_ordinary(dtype, V, one):
+    svd = require_gpu()
+    say(dtype, V, one)
+    z = odd_rows(dtype, V).repeat(11, 1, 1)
+    kw = {n: [V - 1 if n == "k" and x == -1 else x for x in v] * 11 for n, v in ODD[one].items()}
+    check(svd, z, u=np.random.default_rng(one).random((11, 1, 24)), **kw)
+    # the same rows a few at a time are held: the same tokens
+    few = svd.filter_logits(z[:1], **ask(*(None if kw.get(n) is None else kw[n][:1]
+                                           for n in ("t", "k", "p", "least"))))
+    many = svd.filter_logits(z, **ask(*(kw.get(n) for n in ("t", "k", "p", "least"))))
+    same = (few[0] == many[5]) | (few[0].isnan() & many[5].isnan())
+    assert same.all()
