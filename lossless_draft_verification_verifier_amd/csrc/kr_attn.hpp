@@ -716,6 +716,7 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
   // What follows reads its arguments again: held in registers all the way, they spill the
   // loop's own scalars (68 of them, 90 with shaped scores).
   typedef __attribute__((address_space(4))) const char *kernarg;
+  static_assert(alignof(AttnArgs) == 8 && alignof(CacheView) == 8, "where they lie");
   kernarg late = (kernarg)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(late));
   const CacheView &cz = *(const CacheView *)late;

@@ -164,6 +164,8 @@ int shared_kind(const svd_cache_t *cache, const CacheView &c, const AttnArgs &a,
                                : shared_rows<128, false>(c, a, G, o, ms, s);
 }
 
+constexpr float kMostCap = 16384.0f;
+
 struct PrefixLayout {
   size_t seqs, groups, cut, nodes, share_o, share_ms, part_o, part_ms, total;
 };
@@ -370,12 +372,13 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
   if (rc != SVD_OK) return rc;
   if ((share_off != nullptr) != (n_groups > 0)) return SVD_EINVAL;
   if (slopes && anc && !depth) return SVD_EINVAL;  // a tree's distances need its depths
-  if (!(std::isfinite(cap) && cap >= 0.0f)) return SVD_EINVAL;
+  // the tanh of a capped score is off by a few 2^-24 of the cap: past kMostCap by too much
+  if (!(cap >= 0.0f && cap <= kMostCap)) return SVD_EINVAL;
   float cap_in = 0.0f, cap_out = 0.0f;
   if (cap > 0.0f) {
     cap_in = (float)(2.0 * 1.4426950408889634 * (double)scale / (double)cap);
     cap_out = (float)(1.4426950408889634 * (double)cap);
-    if (!(std::isfinite(cap_in) && cap_in > 0.0f && std::isfinite(2.0f * cap_out)))
+    if (!(std::isnormal(cap_in) && std::isnormal(cap_out)))
       return SVD_EINVAL;
   }
   PrefixLayout l;

@@ -141,6 +141,14 @@ def test_prefix_attention_refusals(svd, kw, want):
     assert attend(svd, cache(svd), **kw) == want
 
 
+@pytest.mark.parametrize("cap,scale,want", [
+    (16384.0, 0.125, -3), (16385.0, 0.125, -1), (1e6, 0.125, -1), (1e30, 0.125, -1),
+    (2.0 ** -10, 0.125, -3), (16384.0, 1e-35, -1), (1e-30, 1e30, -1)])
+def test_prefix_attention_refuses_caps_it_cannot_keep(svd, cap, scale, want):
+    # scores would be off by a few 2^-24 of the cap; or scale / cap is no normal number
+    assert attend(svd, cache(svd), cap=cap, scale=scale) == want
+
+
 @pytest.mark.parametrize("kw,want", [
     (dict(k=None), -1), (dict(block_table=None), -1), (dict(dtype=2), -2), (dict(dtype=1), -1),
     (dict(head_dim=96), -1), (dict(page=8), -1), (dict(max_pages=0), -1), (dict(kv_heads=0), -1)])

@@ -236,3 +236,18 @@ def test_many_rows_out_of_the_ordinary(dtype, V, one):
     many = svd.filter_logits(z, **ask(*(kw.get(n) for n in ("t", "k", "p", "least"))))
     same = (few[0] == many[5]) | (few[0].isnan() & many[5].isnan())
     assert same.all()
+
+
+@DTYPES
+@lengths(1009, 8201, 20000, 100008)
+def test_rows_out_of_the_ordinary_in_place(dtype, V):
+    svd = require_gpu()
+    say(dtype, V)
+    z = odd_rows(dtype, V)
+    for one in (dict(), dict(top_k=[10]), dict(top_p=[0.5]), dict(temperature=[0.7], min_p=[0.3])):
+        kw = {n: (torch.tensor(x, device="cuda") if n != "top_k" else
+                  torch.tensor(x, dtype=torch.int32, device="cuda")) for n, x in one.items()}
+        want = svd.filter_logits(z, **kw)
+        same = z.clone()
+        svd.filter_logits(same, out=same, **kw)
+        assert ((same == want) | (same.isnan() & want.isnan())).all()
