@@ -14,7 +14,10 @@
 // a row is divided can change a result; the rounding is 2^-45 of the largest weight at
 // V = 152064, less than what fp64 sums of that many terms lose.
 //
-// One workgroup per row.
+// One workgroup per row.  These passes take any row; kr_filter_row.hpp's are faster but for
+// more than 256 rows of a small vocabulary, where four of these share a CU: 8192 rows of 2048
+// bf16 tokens, top-k and top-p, in 218 us, 67 MB moved.  The searches' LDS counts and scans, one
+// after another, bound them, not the bytes.
 #pragma once
 
 #include "kr_draw.hpp"
