@@ -568,7 +568,9 @@ int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int3
  * the pages that the block tables of all of its sequences begin with are read and
  * multiplied once for the group.  What is computed does not depend on the grouping, but
  * for roundings; sequences outside every group, groups that have no page in common and
- * offsets out of order share nothing.
+ * offsets out of order share nothing.  A hint costs up to four launches more and about
+ * 15 us: calls of a few sequences, or over a few hundred shared tokens, are faster without
+ * groups, and groups of two sequences are not faster at any length.
  * Scores: z = scale * q . k becomes cap * tanh(z / cap) when cap > 0, and then loses
  * slopes[h] * distance when slopes [q_heads] is not NULL, the distance being the row's
  * position less the token's; node t is at position ctx_len[b] + depth[b][t] (depth
@@ -578,7 +580,10 @@ int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int3
  * up to 2^-21 of the cap).  Workspace:
  * svd_prefix_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_pages *
  * page, n_groups) bytes (0 for sizes out of range: also n_groups > B, or, with groups,
- * B * T * q_heads / kv_heads of 2^31 or more), 256-byte aligned.
+ * B * T * q_heads / kv_heads of 2^31 or more), 256-byte aligned.  Groups take head_dim + 2
+ * floats for every row of their tiles: (n + n_groups) * kv_heads + 256 tiles of m rows at
+ * most, n = B * T * q_heads / kv_heads / m, m = 64 where there are no more than 64 rows
+ * B * T * q_heads / kv_heads per group, else 256.
  */
 size_t svd_prefix_attention_workspace_bytes(int64_t B, int32_t T, int32_t q_heads,
                                             int32_t kv_heads, int32_t head_dim, int64_t max_len,

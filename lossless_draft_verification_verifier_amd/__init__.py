@@ -1339,7 +1339,8 @@ def prefix_attention(q, cache, block_table, ctx_len, share_off=None, anc=None, n
     """tree_attention for batches that share prefixes, and for scores that are capped or
     fall off with distance.  share_off [groups+1] int32: sequences share_off[g] to
     share_off[g+1] - 1 are a group, and the pages that all of their block tables begin
-    with are read once for the group; what is computed does not depend on it.  cap: scores
+    with are read once for the group; what is computed does not depend on it (few sequences,
+    or few shared tokens, are faster without).  cap: scores
     become cap * tanh(score / cap) (0 or None: as they are; 16384 at most).  slopes [q_heads] fp32: a
     score loses slopes[h] times the distance between the two positions, a node's position
     being ctx_len[b] + its depth (depth [B,T] int32, needed with anc).  The rest as for

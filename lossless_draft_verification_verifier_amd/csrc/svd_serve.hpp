@@ -127,11 +127,15 @@ int filter_rows(const void *logits, void *out, const FilterArgs &a, int64_t rows
 }
 
 // Rows of a workgroup of the shared part: 256, or 64 with the tokens split over its waves
-// where there are no more.  Whole calls, 4 sequences of a token, 32 query and 8 kv heads: over
-// 32000 shared bf16 tokens 56 us with 64 rows and 66 with 256, over 8192 34 and 37, over 1024
-// 28 either way.
-int share_rows(int64_t B, int32_t T, int64_t group) {
-  return B * T * group <= 64 ? SharedShape<128, 4, 2>::M : SharedShape<128, 8, 1>::M;
+// where groups have no more on average (the host knows no group's own length, and a tile has
+// rows of one group alone).  Whole calls with 32 query and 8 kv heads of 128, one token a
+// sequence, 64 rows against 256: 4 sequences over 32000 shared bf16 tokens 56 and 66 us, over
+// 8192 34 and 37, over 1024 28 either way; 64 groups of 2, 4 and 8 sequences over 8192 shared
+// E4M3 tokens each 437 and 612, 471 and 640, 525 and 694, in workspaces of 28 to 34 MB and of
+// 104 to 111.
+int share_rows(int64_t B, int32_t T, int64_t group, int64_t G) {
+  constexpr int few = SharedShape<128, 4, 2>::M, many = SharedShape<128, 8, 1>::M;
+  return B * T * group <= few * G ? few : many;
 }
 
 template <int D, bool kE4M3, int NW, int WT>
@@ -184,7 +188,7 @@ bool prefix_layout(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int
   };
   if (G > 0) {
     if (B * T >= ((int64_t)1 << 31) / group) return false;
-    const int64_t rows = share_rows(B, T, group);
+    const int64_t rows = share_rows(B, T, group, G);
     // every unit, and every piece of the line, begins a part at most
     const int64_t units = (B * T * group / rows + G) * Hkv;
     if (units >= (int64_t)1 << 30) return false;
@@ -410,7 +414,7 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
     sh.page_shift = c.page_shift;
     sh.group = a.group;
     sh.heads = c.Hkv;
-    sh.m_rows = share_rows(B, T, a.group);
+    sh.m_rows = share_rows(B, T, a.group, n_groups);
     sh.tile = kSharedTile;
     sh.seqs = reinterpret_cast<ShareSeq *>(ws + l.seqs);
     sh.nodes = reinterpret_cast<int32_t *>(ws + l.nodes);
