@@ -49,6 +49,8 @@
 // (prefix, head) pairs; kr_attn_join merges the S parts.
 #pragma once
 
+#include <type_traits>
+
 #include "kr_cache.hpp"
 #include "kr_tree.hpp"
 #include "svd_device.hpp"
@@ -111,6 +113,10 @@ struct AttnArgs {
   const float *share_o;     // [parts][share_rows][D]
   const float *share_ms;    // [parts][share_rows][2]
   int share_rows;
+};
+struct AttnCall {
+  CacheView cache;
+  AttnArgs args;
 };
 
 __device__ __forceinline__ f32x4 mfma_bf16(const vec16 &a, const vec16 &b, const f32x4 &c) {
@@ -259,7 +265,9 @@ enum AttnForm { kTree = 0, kShaped = 1 };
 template <int D, bool kE4M3, int NT, int WQ, int WT, int kForm>
 __global__ __launch_bounds__((AttnShape<D, kE4M3, NT, WQ, WT>::kBlock),
                              (AttnShape<D, kE4M3, NT, WQ, WT>::kMinWaves))
-void kr_tree_attention(CacheView cv, AttnArgs a) {
+void kr_tree_attention(AttnCall call) {
+  const CacheView &cv = call.cache;
+  const AttnArgs &a = call.args;
   constexpr bool kShape = kForm == kShaped;
   using Shape = AttnShape<D, kE4M3, NT, WQ, WT>;
   constexpr int TK = Shape::TK, M = Shape::M, PF = Shape::PF;
@@ -716,12 +724,15 @@ void kr_tree_attention(CacheView cv, AttnArgs a) {
 
   // What follows reads its arguments again: held in registers all the way, they spill the
   // loop's own scalars (68 of them, 90 with shaped scores).
+  // The call is the kernel's one parameter, so its arguments begin with it.
+  static_assert(std::is_same_v<decltype(&kr_tree_attention<D, kE4M3, NT, WQ, WT, kForm>),
+                               void (*)(AttnCall)>, "the arguments are one AttnCall");
   typedef __attribute__((address_space(4))) const char *kernarg;
-  static_assert(alignof(AttnArgs) == 8 && alignof(CacheView) == 8, "where they lie");
   kernarg late = (kernarg)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(late));
-  const CacheView &cz = *(const CacheView *)late;
-  const AttnArgs &az = *(const AttnArgs *)(late + (sizeof(CacheView) + 7) / 8 * 8);
+  const AttnCall &again = *(const AttnCall *)late;
+  const CacheView &cz = again.cache;
+  const AttnArgs &az = again.args;
 
   // one row's 4 elements from d on, its exponent and its sum
   auto put = [&](int R, int d, f32x4 x, float mm, float ll) {

@@ -208,7 +208,7 @@ int attn_launch(const CacheView &c, const AttnArgs &a, int Hq, hipStream_t s) {
   CallTimer tm;
   const int64_t grid = ((int64_t)a.units + 7) / 8 * 8 * a.m_tiles;
   SVD_LAUNCH(tm, SVD_KERNEL_TREE_ATTENTION, s, kr_tree_attention<D, kE4M3, NT, WQ, WT, kForm>,
-             dim3((unsigned)grid), dim3(AttnShape<D, kE4M3, NT, WQ, WT>::kBlock), s, c, a);
+             dim3((unsigned)grid), dim3(AttnShape<D, kE4M3, NT, WQ, WT>::kBlock), s, AttnCall{c, a});
   if (a.S > 1) {
     constexpr int rows = kAttnJoinBlock / (D / 4);
     SVD_LAUNCH(tm, SVD_KERNEL_ATTENTION_JOIN, s, kr_attn_join<D>,
