@@ -522,8 +522,7 @@ int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
 
 /*
  * Filtered logits: the tokens of a row of logits [B][T][V] that its prefix's settings
- * keep, before a verification call (which is lossless for the filtered laws then) or a
- * draw.  With w = exp((z - max z) / temperature[b]) kept are, in this order,
+ * keep, before a verification call or a draw.  With w = exp((z - max z) / temperature[b]) kept are, in this order,
  *   the tokens with w >= min_p[b] (0 or less: all; the largest logit always);
  *   of those the first top_k[b] by falling logit, the lower index first among equal
  *     ones (0 or less, or at least V: all);
@@ -538,6 +537,11 @@ int svd_adjust_logits(const void *logits, void *out, svd_dtype_t dtype, int64_t 
  * svd_filter_logits: out [B][T][V] holds the logits as they are, not divided by the
  * temperature, and -inf for every token that is not kept.  out may be logits itself, but
  * must not overlap it otherwise.
+ * A verification call on these rows is lossless for the filtered laws where its temp_p
+ * (temp_q for a drafter's rows) is temperature[b].  It takes one for its whole batch: prefixes
+ * of other temperatures go to calls of their own, with their row_base, or their fp32 logits
+ * are divided first, and are filtered without a temperature and verified at 1.  A prefix whose
+ * temperature is 0 keeps one token and goes with any.
  *
  * svd_sample: K tokens per row, for K drafts of one set of marginals.  token [B][K][T]
  * out: the first token by index up to which the kept weights exceed u times their sum;
@@ -568,8 +572,8 @@ int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int3
  * the pages that the block tables of all of its sequences begin with are read and
  * multiplied once for the group.  What is computed does not depend on the grouping, but
  * for roundings; sequences outside every group, groups that have no page in common and
- * offsets out of order share nothing.  A hint costs up to four launches more and about
- * 15 us: calls of a few sequences, or over a few hundred shared tokens, are faster without
+ * offsets out of order share nothing.  A hint costs two or three launches more, about 15
+ * us: calls of a few sequences, or over a few hundred shared tokens, are faster without
  * groups, and groups of two sequences are not faster at any length.
  * Scores: z = scale * q . k becomes cap * tanh(z / cap) when cap > 0, and then loses
  * slopes[h] * distance when slopes [q_heads] is not NULL, the distance being the row's

@@ -1277,8 +1277,11 @@ def filter_logits(logits, temperature=None, top_k=None, top_p=None, min_p=None, 
     less: all), top_p the shortest beginning of that order that holds top_p of their
     weight.  temperature, top_p, min_p [B] fp32, top_k [B] int32, each or None; a
     temperature of 0 keeps the first most likely token alone.  The logits themselves are
-    not divided by the temperature.  n_rows [B]: rows from n_rows[b] on are left as out has
-    them.  out: default a new tensor; logits itself for a change in place.  Returns out."""
+    not divided by the temperature: a verification is lossless for the filtered laws where its
+    temp_p (temp_q for a drafter's rows) is the prefix's temperature, and it has one for its
+    batch, so prefixes of other temperatures go to calls of their own, or fp32 logits are
+    divided first, filtered without a temperature and verified at 1.  n_rows [B]: rows from
+    n_rows[b] on are left as out has them.  out: default a new tensor; logits itself for a change in place.  Returns out."""
     if stream is not None:
         return _on(stream, logits, filter_logits, logits, temperature, top_k, top_p, min_p, n_rows,
                    out)
