@@ -202,8 +202,9 @@ __device__ __forceinline__ ShareRow share_row(const AttnArgs &a, int64_t b, int 
   return ShareRow{(g.unit0 + unit + w0) * a.share_rows + R % a.share_rows, (int)(w1 - w0) + 1};
 }
 // 4 elements of a row's own part (exponent m, sum l) joined by those of its shared parts, kAhead
-// of them on their way at a time: one or two behind a long loop, up to 16 where few rows made
-// many parts (a single token behind a shared prefix: 9.2 us with one, 5.7 with eight).
+// of them on their way at a time: one or two behind a long loop; where few rows made many parts,
+// one per piece of the line that their unit meets, 256 at most (8 for a single token behind 1024
+// shared ones, of 8 kv heads: 9.2 us with one on its way, 5.7 with eight).
 template <int D, int kAhead>
 __device__ __forceinline__ void share_join(const AttnArgs &a, const ShareRow &r, int d, f32x4 &o,
                                            float &m, float &l) {
