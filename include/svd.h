@@ -581,7 +581,7 @@ int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int3
  * [B][T], needed with slopes and anc; without anc, for a chain, it is not read).
  * Everything else is as for svd_tree_attention, whose results a call without groups, cap and
  * slopes gives bit for bit.  cap is from 0 to 16384 (in fp32 a capped score is off by
- * up to 2^-21 of the cap).  Workspace:
+ * up to 2^-21 of the cap), 2 log2(e) scale / cap a normal fp32 number.  Workspace:
  * svd_prefix_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_pages *
  * page, n_groups) bytes (0 for sizes out of range: also n_groups > B, or, with groups,
  * B * T * q_heads / kv_heads of 2^31 or more), 256-byte aligned.  Groups take head_dim + 2

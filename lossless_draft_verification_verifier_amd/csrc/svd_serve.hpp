@@ -376,7 +376,7 @@ int svd_prefix_attention(const svd_cache_t *cache, const void *q, int64_t q_stri
   if (rc != SVD_OK) return rc;
   if ((share_off != nullptr) != (n_groups > 0)) return SVD_EINVAL;
   if (slopes && anc && !depth) return SVD_EINVAL;  // a tree's distances need its depths
-  // the tanh of a capped score is off by a few 2^-24 of the cap: past kMostCap by too much
+  // a capped score is off by up to 2^-21 of the cap, 2^-7 at kMostCap: past it by too much
   if (!(cap >= 0.0f && cap <= kMostCap)) return SVD_EINVAL;
   float cap_in = 0.0f, cap_out = 0.0f;
   if (cap > 0.0f) {
