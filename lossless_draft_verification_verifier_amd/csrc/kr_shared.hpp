@@ -11,15 +11,24 @@
 // waves a workgroup, two a SIMD, one workgroup per CU.  With 16 rows of a wave the reads of
 // K and V from LDS are what bounds it (141 us for 256 sequences of 9 nodes, 32 query and 8 kv
 // heads, over 2048 shared E4M3 tokens), with 64 rows and one wave per SIMD the issue of one
-// wave's instructions (125 us); 32 rows and two waves take 92 us, 840 TFLOP/s, where a large
-// library product reaches 1328.  Capped scores bind the vector units: 210 GFLOP (32 trees of
-// 17 to 33 nodes over 16000 bf16 tokens of four groups) in 343 us, 610 TFLOP/s.
+// wave's instructions (125 us); 32 rows and two waves take 92 us (97 on another card), 840
+// TFLOP/s, where a large library product reaches 1328.  Capped scores bind the vector units:
+// 210 GFLOP (32 trees of 17 to 33 nodes over 16000 bf16 tokens of four groups) in 344 us (358),
+// 610 TFLOP/s.
+//
+// p is rounded to bf16 once, as the operand of the second product, by at most 2^-8 of itself;
+// m, l and O stay in 32 bits and l sums the unrounded p.  That is a choice, the same as in
+// kr_attn.hpp: outputs of random values are off by 0.0021 (the trees) to 0.0022 (the batch) of
+// their norm, where their own rounding to bf16 alone makes 0.0017.  With the rest of p as a
+// second operand they are off by 0.0017 and 0.0018 (the batch's own part still rounds its p),
+// and whole calls take 309 instead of 285 us for the batch and 493 instead of 420 for the trees.
+//
 // Inside a wave the steps are laid side by side: a block of 32 tokens is exponentiated
 // while the next block's scores are computed, and its values meet their p a block later,
 // while the maxima of the next one are taken.
 //
-// Few rows (64 at most, of one group's sequences) leave six of the eight waves idle; then
-// four waves share 64 rows, two and two with half of the tokens each.
+// Few rows of a group (64 at most) would leave six of the eight waves idle; then four waves share
+// 64 rows, two and two with half of the tokens each.
 //
 // K and V tiles lie in LDS as they are in memory, bf16 rows (widened on the way from E4M3,
 // exactly); V^T comes from a transposing read, four tokens of one head element per lane.
