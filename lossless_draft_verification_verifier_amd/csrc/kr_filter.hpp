@@ -91,8 +91,8 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long x,
   return before + up - x;
 }
 
-// The logits of a row, visited in index order by 8 * kFilterBlock tokens at a time:
-// f(index, value) for every token.
+// The logits of a row, f(index, value) for every token: with kVec a 16-byte piece of P tokens
+// per thread and NT * P at a time, else one per thread and NT at a time.
 template <typename E, bool kVec, int NT, typename F>
 __device__ __forceinline__ void filter_visit(const typename E::elem *row, int64_t lo, int64_t hi,
                                              F &&f) {

@@ -73,6 +73,10 @@ int filter_args(FilterArgs &a, svd_dtype_t dtype, int64_t B, int32_t T, int32_t 
 // workgroups share a CU.  Top-k and top-p of bf16, held against passes: one row of 8192 12
 // against 37 us, of 512 11 against 20; 256 rows of 8192 17 against 39, of 512 16 against 21;
 // 2048 rows of 8192 115 against 110, of 512 100 against 55; 8192 rows of 2048 405 against 218.
+// Above 8192 tokens a row is held whatever the number of rows: 8192 rows of 16384 463 against
+// 633, 2304 of 32000 154 against 357 (fp32 333 against 683), 512 of 64000 49 against 214.  Top-p
+// alone: 507 against 526, 165 against 290 (322 against 470), 52 against 180; 8192 rows of 8193, at
+// the border, 561 against 498.
 constexpr int64_t kFilterSmall = 8192, kFilterRound = 256;  // tokens; rows, one per CU
 
 template <typename E, int NV>
