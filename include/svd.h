@@ -573,8 +573,9 @@ int svd_sample(const void *logits, svd_dtype_t dtype, int64_t B, int32_t T, int3
  * multiplied once for the group.  What is computed does not depend on the grouping, but
  * for roundings; sequences outside every group, groups that have no page in common and
  * offsets out of order share nothing.  A hint costs two or three launches more, about 15
- * us: calls of a few sequences, or over a few hundred shared tokens, are faster without
- * groups, and groups of two sequences are not faster at any length.
+ * us: calls of a few sequences, and most over a few hundred shared tokens, are faster
+ * without groups, and so are groups of two sequences of one token each (up to 8192 shared
+ * ones measured).
  * Scores: z = scale * q . k becomes cap * tanh(z / cap) when cap > 0, and then loses
  * slopes[h] * distance when slopes [q_heads] is not NULL, the distance being the row's
  * position less the token's; node t is at position ctx_len[b] + depth[b][t] (depth
